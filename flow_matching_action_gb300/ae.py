@@ -20,6 +20,8 @@ AE_WEIGHTS_AS_DTYPE = 0
 AE_WEIGHTS_FP8_E4M3 = 1
 AE_MAX_BATCH = 64
 AE_MAX_STEPS = 128
+AE_MAX_AXES = 4
+AE_MAX_TOKENS = 65535
 
 STATUS_NAMES = {0: "AE_OK", -1: "AE_ERR_INVALID_ARG", -2: "AE_ERR_SHAPE", -3: "AE_ERR_NOT_BOUND",
                 -4: "AE_ERR_CUDA", -5: "AE_ERR_DEVICE", -6: "AE_ERR_OOM", -7: "AE_ERR_UNSUPPORTED"}
@@ -55,6 +57,32 @@ class ae_info(ctypes.Structure):
                 ("device_bytes", ctypes.c_int64), ("sm_count", ctypes.c_int), ("path", ctypes.c_int)]
 
 
+class ae_qk_norm_rope_args(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int), ("n_axes", ctypes.c_int), ("qkv", ctypes.c_void_p),
+                ("qkv_stride", ctypes.c_int64), ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p),
+                ("norm_offset", ctypes.c_float), ("positions", ctypes.c_void_p),
+                ("pair_axis", ctypes.c_char_p), ("pair_freq", ctypes.c_void_p),
+                ("kv_rows", ctypes.c_void_p), ("cache_rows", ctypes.c_int64), ("q_out", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+                ("kv_stride", ctypes.c_int64)]
+
+
+class ae_prompt_attention_args(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("causal", ctypes.c_int), ("cu_q", ctypes.c_void_p),
+                ("kv_row0", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("cache_rows", ctypes.c_int64),
+                ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64), ("k", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("kv_stride", ctypes.c_int64), ("key_mask", ctypes.c_void_p),
+                ("scale", ctypes.c_float), ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64)]
+
+
+class ae_token_attention_args(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("max_len", ctypes.c_int), ("kv_row0", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("cache_rows", ctypes.c_int64), ("q", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("kv_stride", ctypes.c_int64), ("key_mask", ctypes.c_void_p), ("scale", ctypes.c_float),
+                ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64)]
+
+
 # Every symbol include/ae.h declares, with its ctypes signature.
 _SIGNATURES = {
     "ae_create": (ctypes.c_int, [ctypes.POINTER(ae_config), ctypes.POINTER(ae_weights), ctypes.c_int,
@@ -68,6 +96,9 @@ _SIGNATURES = {
     "ae_bind_context": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
                                        ctypes.POINTER(ctypes.c_int32), ctypes.c_void_p]),
     "ae_prefill": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "ae_qk_norm_rope": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ae_qk_norm_rope_args)]),
+    "ae_prompt_attention": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ae_prompt_attention_args)]),
+    "ae_token_attention": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ae_token_attention_args)]),
     "ae_sample": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]),
     "ae_sample_noalloc": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]),
     "ae_set_debug_dump": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t]),
@@ -186,6 +217,50 @@ def ae_prefill(ctx, batch: int, embeddings, out_k, out_v) -> None:
     _check(lib().ae_prefill(ctx, batch, _ptr(embeddings), _ptr(out_k), _ptr(out_v)), ctx)
 
 
+def ae_qk_norm_rope(ctx, args: ae_qk_norm_rope_args) -> None:
+    _check(lib().ae_qk_norm_rope(ctx, ctypes.byref(args)), ctx)
+
+
+def ae_prompt_attention(ctx, args: ae_prompt_attention_args) -> None:
+    _check(lib().ae_prompt_attention(ctx, ctypes.byref(args)), ctx)
+
+
+def ae_token_attention(ctx, args: ae_token_attention_args) -> None:
+    _check(lib().ae_token_attention(ctx, ctypes.byref(args)), ctx)
+
+
+def _rows(name: str, t, width: int, rows: Optional[int] = None):
+    """(pointer, row stride) of a bf16 CUDA tensor [rows, width] whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{'rows' if rows is None else rows}, {width}]")
+    if str(t.dtype) != "torch.bfloat16" or not t.is_cuda:
+        raise ValueError(f"{name}: expected a bf16 CUDA tensor, got {t.dtype} on {t.device}")
+    if width > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row must be contiguous")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width  # one row has no stride
+
+
+def _vec(name: str, t, dtype: str, n: int):
+    """Pointer of a contiguous CUDA tensor of n elements, or None."""
+    if t is None:
+        return None
+    if str(t.dtype) != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name}: expected {n} contiguous {dtype} elements on the GPU, got {tuple(t.shape)} "
+                         f"{t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _host_array(ctype, x):
+    """A host array of a sequence (kept as it is when it already is a ctypes array), or None."""
+    if x is None or isinstance(x, ctypes.Array):
+        return x
+    return (ctype * len(x))(*x)
+
+
+def _addr(arr):
+    return None if arr is None else ctypes.addressof(arr)
+
+
 def ae_sample(ctx, noise, n_steps: int, out_actions) -> None:
     _check(lib().ae_sample(ctx, _ptr(noise), n_steps, _ptr(out_actions)), ctx)
 
@@ -260,6 +335,102 @@ class ActionExpert:
         """One request's prefix bound for n_samples samples of the same observation."""
         ae_bind_prefix_shared(self.ctx, n_samples, prefix_k, prefix_v, n_rows, prefix_mask)
         self._bound = (prefix_k, prefix_v, prefix_mask)
+
+    def qk_norm_rope(self, qkv, positions, q_out, k_cache, v_cache, q_norm=None, k_norm=None,
+                     norm_offset: float = 0.0, pair_axis=None, pair_freq=None, kv_rows=None):
+        """Per-head norm, rotation and cache write of merged q|k|v rows (see include/ae.h).
+
+        qkv [tokens, (Hq + 2 Hkv) dh], q_out [tokens, Hq dh], k_cache / v_cache [rows, Hkv dh]: bf16.
+        positions int32 [tokens] or [axes, tokens]; kv_rows int64 [tokens] or None; pair_axis bytes or a
+        sequence of dh / 2 axes; pair_freq a sequence of dh / 2 frequencies.
+        """
+        d = self.dims
+        n = qkv.shape[0]
+        a = ae_qk_norm_rope_args()
+        a.tokens = n
+        a.n_axes = positions.shape[0] if positions.dim() == 2 else 1
+        a.qkv, a.qkv_stride = _rows("qkv", qkv, d.q_dim + 2 * d.kv_dim)
+        a.q_norm = _vec("q_norm", q_norm, "torch.bfloat16", d.head_dim)
+        a.k_norm = _vec("k_norm", k_norm, "torch.bfloat16", d.head_dim)
+        a.norm_offset = norm_offset
+        a.positions = _vec("positions", positions, "torch.int32", a.n_axes * n)
+        half = d.head_dim // 2
+        if pair_axis is not None:
+            if len(pair_axis) != half:
+                raise ValueError(f"pair_axis: {len(pair_axis)} entries, expected {half}")
+            # a bytes object of at least `half` entries; ctypes passes its buffer
+            a.pair_axis = pair_axis if isinstance(pair_axis, bytes) else bytes(pair_axis)
+        freq = _host_array(ctypes.c_double, pair_freq)
+        if freq is not None and len(freq) != half:
+            raise ValueError(f"pair_freq: {len(freq)} entries, expected {half}")
+        a.pair_freq = _addr(freq)
+        a.kv_rows = _vec("kv_rows", kv_rows, "torch.int64", n)
+        a.q_out, a.q_stride = _rows("q_out", q_out, d.q_dim, n)
+        a.k_cache, a.kv_stride = _rows("k_cache", k_cache, d.kv_dim)
+        a.cache_rows = k_cache.shape[0]
+        a.v_cache, v_stride = _rows("v_cache", v_cache, d.kv_dim, k_cache.shape[0])
+        if v_stride != a.kv_stride:
+            raise ValueError("k_cache and v_cache have different row strides")
+        ae_qk_norm_rope(self.ctx, a)
+
+    def prompt_attention(self, q, k, v, cu_q, kv_row0=None, kv_len=None, key_mask=None, causal: bool = True,
+                         scale: float = 0.0, out=None):
+        """Attention of packed prompts (see include/ae.h); returns out [rows, Hq dh].
+
+        q [rows, Hq dh], k / v [cache rows, Hkv dh]: bf16.  cu_q, kv_row0, kv_len are host sequences;
+        key_mask uint8 [cache rows] on the GPU.
+        """
+        d = self.dims
+        if out is None:
+            out = q.new_zeros(q.shape)
+        a = ae_prompt_attention_args()
+        cu = _host_array(ctypes.c_int32, cu_q)
+        row0, lens = _host_array(ctypes.c_int64, kv_row0), _host_array(ctypes.c_int32, kv_len)
+        a.batch = len(cu) - 1
+        for name, x in (("kv_row0", row0), ("kv_len", lens)):
+            if x is not None and len(x) != a.batch:
+                raise ValueError(f"{name}: {len(x)} entries for {a.batch} sequences")
+        if q.shape[0] < cu[a.batch]:
+            raise ValueError(f"q: {q.shape[0]} rows, cu_q ends at {cu[a.batch]}")
+        a.causal = 1 if causal else 0
+        a.cu_q, a.kv_row0, a.kv_len = _addr(cu), _addr(row0), _addr(lens)
+        a.q, a.q_stride = _rows("q", q, d.q_dim)
+        a.k, a.kv_stride = _rows("k", k, d.kv_dim)
+        a.cache_rows = k.shape[0]
+        a.v, v_stride = _rows("v", v, d.kv_dim, k.shape[0])
+        if v_stride != a.kv_stride:
+            raise ValueError("k and v have different row strides")
+        a.key_mask = _vec("key_mask", key_mask, "torch.uint8", a.cache_rows)
+        a.scale = scale
+        a.out, a.out_stride = _rows("out", out, d.q_dim, q.shape[0])
+        ae_prompt_attention(self.ctx, a)
+        return out
+
+    def token_attention(self, q, k, v, kv_row0, kv_len, max_len: int, key_mask=None, scale: float = 0.0, out=None):
+        """Attention of one new token per request over its cached rows (see include/ae.h); returns out.
+
+        q [requests, Hq dh], k / v [cache rows, Hkv dh]: bf16; kv_row0 int64, kv_len int32 [requests] and
+        key_mask uint8 [cache rows] on the GPU.
+        """
+        d = self.dims
+        n = q.shape[0]
+        if out is None:
+            out = q.new_empty(q.shape)
+        a = ae_token_attention_args()
+        a.batch, a.max_len = n, max_len
+        a.kv_row0 = _vec("kv_row0", kv_row0, "torch.int64", n)
+        a.kv_len = _vec("kv_len", kv_len, "torch.int32", n)
+        a.q, a.q_stride = _rows("q", q, d.q_dim)
+        a.k, a.kv_stride = _rows("k", k, d.kv_dim)
+        a.cache_rows = k.shape[0]
+        a.v, v_stride = _rows("v", v, d.kv_dim, k.shape[0])
+        if v_stride != a.kv_stride:
+            raise ValueError("k and v have different row strides")
+        a.key_mask = _vec("key_mask", key_mask, "torch.uint8", a.cache_rows)
+        a.scale = scale
+        a.out, a.out_stride = _rows("out", out, d.q_dim, n)
+        ae_token_attention(self.ctx, a)
+        return out
 
     def sample(self, noise, n_steps: int, out=None):
         if out is None:

@@ -1,6 +1,8 @@
 // C-ABI entry points and host runtime: argument checks, the weight packer,
 // the prefix binder, the per-n_steps time-conditioning table, and the step
 // loop.  No compute happens on the host; every step of the path is a kernel.
+#include <math.h>
+
 #include <cstdarg>
 #include <cstdio>
 #include <cstdlib>
@@ -502,6 +504,8 @@ ae_status ae_create(const ae_config* cfg, const ae_weights* w, int max_batch,
   c->d = Dims{cfg->layers, cfg->width, cfg->mlp, cfg->n_q_heads, cfg->n_kv_heads, cfg->head_dim,
               cfg->action_dim, cfg->horizon, cfg->rms_eps, cfg->rope_theta,
               cfg->time_min_period, cfg->time_max_period, cfg->dtype, cfg->ctx_dim};
+  for (int j = 0; j < c->d.dh / 2; ++j)
+    c->rope_turn[j] = ae::turn_fraction(pow(c->d.theta, -2.0 * j / c->d.dh));
   c->max_batch = max_batch;
   c->max_rows = max_prefix_rows;
   c->stream = (cudaStream_t)stream;
@@ -529,6 +533,7 @@ ae_status ae_create(const ae_config* cfg, const ae_weights* w, int max_batch,
     e = ae::fast_setup(c);
     if (e == cudaSuccess) e = ae::gemm_kernel_setup();
     if (e == cudaSuccess) e = ae::attn_kernel_setup();
+    if (e == cudaSuccess) e = ae::lm_kernel_setup();
     if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&c->cap_stream, cudaStreamNonBlocking);
     if (e != cudaSuccess) st = cuda_fail(c, e, "bf16 path setup");
     // AE_GRAPH=0 / AE_PDL=0 run the same kernels launched one by one / without overlap

@@ -115,6 +115,7 @@ struct ae_ctx {
   ae::BindState bind;
 
   std::vector<ae::TimeTable> tables;
+  uint64_t rope_turn[128] = {0};  // rope_theta^(-2j/dh) per position as a fraction of a turn (ae_qk_norm_rope)
 
   // Sticky device status: host-mapped so it can be read without a sync.
   int* status_host = nullptr;
@@ -338,6 +339,60 @@ cudaError_t make_f32_3d_map(CUtensorMap* map, const void* ptr, long d0, long d1,
 cudaError_t make_attn_o_map(CUtensorMap* map, float* part_o, size_t units, int dh);
 // bf16 [units * 128, dh] view of part_o, boxes of 128 rows x 64 columns, 128-byte swizzle
 cudaError_t make_attn_o16_map(CUtensorMap* map, float* part_o, size_t units, int dh);
+
+// ---- language-model attention operators (ae_lm_ops.cu checks, these launch)
+struct RopeNormArgs {
+  int tokens, n_axes, Hq, Hkv;
+  const bf16* qkv;
+  int64_t qkv_stride;
+  const bf16 *q_norm, *k_norm;
+  float norm_offset, eps;
+  const int32_t* positions;
+  const int64_t* kv_rows;
+  int64_t cache_rows;
+  bf16* q_out;
+  int64_t q_stride;
+  bf16 *k_cache, *v_cache;
+  int64_t kv_stride;
+  int* status;
+  uint64_t turn[128];  // pair_freq / 2 pi as a fraction of a turn, in units of 2^-64
+  uint8_t axis[128];
+};
+// Radians per position as a fraction of a turn in units of 2^-64 (whole turns
+// drop out: positions are integers).
+uint64_t turn_fraction(double radians);
+cudaError_t launch_qk_norm_rope(const RopeNormArgs& a, int dh, int sm_count, cudaStream_t s);
+
+struct PromptAttnArgs {
+  int batch, causal, Hq, Hkv;
+  int64_t cache_rows;
+  const bf16 *q, *k, *v;
+  int64_t q_stride, kv_stride, out_stride;
+  const uint8_t* key_mask;
+  float scale;
+  bf16* out;
+  int* status;
+  int cu_q[AE_MAX_BATCH + 1];
+  int kv_len[AE_MAX_BATCH];
+  int64_t kv_row0[AE_MAX_BATCH];
+};
+cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int dh, int sm_count, cudaStream_t s);
+
+struct TokenAttnArgs {
+  int batch, max_len, Hq, Hkv;
+  const int64_t* kv_row0;
+  const int32_t* kv_len;
+  int64_t cache_rows;
+  const bf16 *q, *k, *v;
+  int64_t q_stride, kv_stride, out_stride;
+  const uint8_t* key_mask;
+  float scale;
+  bf16* out;
+  int* status;
+};
+cudaError_t launch_token_attention(const TokenAttnArgs& a, int dh, int sm_count, cudaStream_t s);
+// Kernel attributes (shared memory), once per context.
+cudaError_t lm_kernel_setup();
 
 // ---- context projection (ae_bind_context)
 // ctx_rope[valid row of request b at position i] = (cos, sin)(i theta^(-2j/dh)).

@@ -1,0 +1,255 @@
+// Entry points of the language-model attention operators: argument checks and
+// the launch arguments.  Everything a caller can get wrong on the host is
+// refused here, before any CUDA call.
+#include <math.h>
+#include <stdarg.h>
+#include <stdio.h>
+
+#include "ae_internal.h"
+
+namespace {
+
+ae_status fail(ae_ctx* c, ae_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof(buf), fmt, ap);
+  va_end(ap);
+  c->last_msg = buf;
+  return st;
+}
+
+#define AE_TRY(expr)                 \
+  do {                               \
+    const ae_status s_ = (expr);     \
+    if (s_ != AE_OK) return s_;      \
+  } while (0)
+
+// bf16 rows of `width` elements: 16-byte aligned base, stride a multiple of 8 and >= width.
+ae_status check_rows(ae_ctx* c, const char* name, const void* p, int64_t stride, int64_t width) {
+  if (p == nullptr) return fail(c, AE_ERR_INVALID_ARG, "%s is NULL", name);
+  if ((uintptr_t)p % 16 != 0) return fail(c, AE_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  if (stride < width)
+    return fail(c, AE_ERR_SHAPE, "%s: row stride %lld < row length %lld", name, (long long)stride, (long long)width);
+  if (stride % 8 != 0)
+    return fail(c, AE_ERR_INVALID_ARG, "%s: row stride %lld is not a multiple of 8", name, (long long)stride);
+  // a TMA row stride has 40 bits
+  if (stride > ((int64_t)1 << 38))
+    return fail(c, AE_ERR_SHAPE, "%s: row stride %lld is too large", name, (long long)stride);
+  return AE_OK;
+}
+
+// Row counts travel as 32-bit TMA coordinates.
+ae_status check_cache_rows(ae_ctx* c, int64_t rows) {
+  if (rows < 0 || rows > 0x7fffff00LL)
+    return fail(c, AE_ERR_SHAPE, "cache_rows %lld outside 0..%lld", (long long)rows, 0x7fffff00LL);
+  return AE_OK;
+}
+
+ae_status check_scale(ae_ctx* c, float scale) {
+  if (!(scale >= 0.f) || isinf(scale)) return fail(c, AE_ERR_INVALID_ARG, "scale must be finite and >= 0");
+  return AE_OK;
+}
+
+// Checks common to the operators.  `op` names the call.
+ae_status check_context(ae_ctx* c, const void* args, const char* op) {
+  if (args == nullptr) return fail(c, AE_ERR_INVALID_ARG, "%s: args is NULL", op);
+  if (!c->fast) return fail(c, AE_ERR_UNSUPPORTED, "%s runs on bf16 contexts only", op);
+  if (c->status_host && *(volatile int*)c->status_host)
+    return fail(c, AE_ERR_DEVICE, "a device-side check failed earlier (code %d)", *c->status_host);
+  return AE_OK;
+}
+
+// The last check: the first CUDA call.
+ae_status check_device(ae_ctx* c) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return fail(c, AE_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+  if (dev != c->device)
+    return fail(c, AE_ERR_INVALID_ARG, "device %d is current, the context lives on device %d", dev, c->device);
+  return AE_OK;
+}
+
+ae_status launched(ae_ctx* c, cudaError_t e, const char* op) {
+  if (e != cudaSuccess) return fail(c, AE_ERR_CUDA, "%s launch: %s", op, cudaGetErrorString(e));
+  return AE_OK;
+}
+
+}  // namespace
+
+namespace ae {
+
+uint64_t turn_fraction(double radians) {
+  const double turns = radians * 0.15915494309189533577;  // 1 / (2 pi)
+  const double frac = turns - floor(turns);               // whole turns drop out
+  // frac in [0, 1]; 2^64 itself wraps to 0
+  const double hi = floor(frac * 4294967296.0);
+  const double lo = (frac * 4294967296.0 - hi) * 4294967296.0;
+  return ((uint64_t)hi << 32) + (uint64_t)lo;
+}
+
+}  // namespace ae
+
+extern "C" {
+
+ae_status ae_qk_norm_rope(ae_ctx* c, const ae_qk_norm_rope_args* p) {
+  if (c == nullptr) return AE_ERR_INVALID_ARG;
+  const char* op = "ae_qk_norm_rope";
+  AE_TRY(check_context(c, p, op));
+  const ae::Dims& d = c->d;
+  if (p->tokens < 0) return fail(c, AE_ERR_SHAPE, "tokens %d < 0", p->tokens);
+  if (p->n_axes < 1 || p->n_axes > AE_MAX_AXES)
+    return fail(c, AE_ERR_SHAPE, "n_axes %d outside 1..%d", p->n_axes, AE_MAX_AXES);
+  if (!isfinite(p->norm_offset)) return fail(c, AE_ERR_INVALID_ARG, "norm_offset must be finite");
+  AE_TRY(check_cache_rows(c, p->cache_rows));
+  if (p->pair_axis != nullptr)
+    for (int j = 0; j < d.dh / 2; ++j)
+      if (p->pair_axis[j] >= p->n_axes)
+        return fail(c, AE_ERR_INVALID_ARG, "pair_axis[%d] = %d, n_axes is %d", j, p->pair_axis[j], p->n_axes);
+  if (p->pair_freq != nullptr)
+    for (int j = 0; j < d.dh / 2; ++j)
+      if (!isfinite(p->pair_freq[j])) return fail(c, AE_ERR_INVALID_ARG, "pair_freq[%d] is not finite", j);
+  if (p->tokens == 0) return AE_OK;
+  if (p->kv_rows == nullptr && p->tokens > p->cache_rows)
+    return fail(c, AE_ERR_SHAPE, "%d tokens, %lld cache rows", p->tokens, (long long)p->cache_rows);
+  AE_TRY(check_rows(c, "qkv", p->qkv, p->qkv_stride, d.qkvdim()));
+  AE_TRY(check_rows(c, "q_out", p->q_out, p->q_stride, d.qdim()));
+  AE_TRY(check_rows(c, "k_cache", p->k_cache, p->kv_stride, d.kvdim()));
+  AE_TRY(check_rows(c, "v_cache", p->v_cache, p->kv_stride, d.kvdim()));
+  if (p->q_out == p->qkv && p->q_stride != p->qkv_stride)
+    return fail(c, AE_ERR_INVALID_ARG, "q_out is qkv but the row strides differ");
+  for (const void* w : {p->q_norm, p->k_norm})
+    if ((uintptr_t)w % 16 != 0) return fail(c, AE_ERR_INVALID_ARG, "a norm weight is not 16-byte aligned");
+  if (p->positions == nullptr) return fail(c, AE_ERR_INVALID_ARG, "positions is NULL");
+  if ((uintptr_t)p->positions % 4 != 0 || (uintptr_t)p->kv_rows % 8 != 0)
+    return fail(c, AE_ERR_INVALID_ARG, "positions / kv_rows is not aligned to its elements");
+  AE_TRY(check_device(c));
+  ae::RopeNormArgs a;
+  a.tokens = p->tokens;
+  a.n_axes = p->n_axes;
+  a.Hq = d.Hq;
+  a.Hkv = d.Hkv;
+  a.qkv = (const ae::bf16*)p->qkv;
+  a.qkv_stride = p->qkv_stride;
+  a.q_norm = (const ae::bf16*)p->q_norm;
+  a.k_norm = (const ae::bf16*)p->k_norm;
+  a.norm_offset = p->norm_offset;
+  a.eps = (float)d.eps;
+  a.positions = p->positions;
+  a.kv_rows = p->kv_rows;
+  a.cache_rows = p->cache_rows;
+  a.q_out = (ae::bf16*)p->q_out;
+  a.q_stride = p->q_stride;
+  a.k_cache = (ae::bf16*)p->k_cache;
+  a.v_cache = (ae::bf16*)p->v_cache;
+  a.kv_stride = p->kv_stride;
+  a.status = c->status_dev;
+  for (int j = 0; j < d.dh / 2; ++j) {
+    a.axis[j] = p->pair_axis ? p->pair_axis[j] : 0;
+    a.turn[j] = p->pair_freq ? ae::turn_fraction(p->pair_freq[j]) : c->rope_turn[j];
+  }
+  return launched(c, ae::launch_qk_norm_rope(a, d.dh, c->sm_count, c->stream), op);
+}
+
+ae_status ae_prompt_attention(ae_ctx* c, const ae_prompt_attention_args* p) {
+  if (c == nullptr) return AE_ERR_INVALID_ARG;
+  const char* op = "ae_prompt_attention";
+  AE_TRY(check_context(c, p, op));
+  const ae::Dims& d = c->d;
+  if (p->batch < 0 || p->batch > AE_MAX_BATCH)
+    return fail(c, AE_ERR_SHAPE, "batch %d outside 0..%d", p->batch, AE_MAX_BATCH);
+  AE_TRY(check_scale(c, p->scale));
+  AE_TRY(check_cache_rows(c, p->cache_rows));
+  if (p->batch == 0) return AE_OK;
+  if (p->cu_q == nullptr) return fail(c, AE_ERR_INVALID_ARG, "cu_q is NULL");
+  if ((p->kv_row0 == nullptr) != (p->kv_len == nullptr))
+    return fail(c, AE_ERR_INVALID_ARG, "kv_row0 and kv_len come together");
+  if (p->cu_q[0] != 0) return fail(c, AE_ERR_SHAPE, "cu_q[0] must be 0");
+  ae::PromptAttnArgs a;
+  for (int b = 0; b < p->batch; ++b) {
+    const int64_t n = (int64_t)p->cu_q[b + 1] - p->cu_q[b];
+    if (n < 0) return fail(c, AE_ERR_SHAPE, "cu_q decreases at sequence %d", b);
+    const int64_t r0 = p->kv_row0 ? p->kv_row0[b] : p->cu_q[b];
+    const int64_t m = p->kv_len ? p->kv_len[b] : n;
+    if (m < n)
+      return fail(c, AE_ERR_SHAPE, "sequence %d has %lld queries but %lld keys", b, (long long)n, (long long)m);
+    // m - n keys without queries are never read, but a range is a range
+    if (r0 < 0 || r0 > p->cache_rows || m > p->cache_rows - r0)
+      return fail(c, AE_ERR_SHAPE, "sequence %d: cache rows %lld .. +%lld outside 0..%lld", b, (long long)r0,
+                  (long long)m, (long long)p->cache_rows);
+    a.cu_q[b] = p->cu_q[b];
+    a.kv_row0[b] = r0;
+    a.kv_len[b] = (int)m;
+  }
+  a.cu_q[p->batch] = p->cu_q[p->batch];
+  const int total = p->cu_q[p->batch];
+  if (total == 0) return AE_OK;
+  if ((int64_t)total * (d.Hq / d.Hkv) > 0x7fffff00LL)
+    return fail(c, AE_ERR_SHAPE, "%d query rows are too many", total);
+  AE_TRY(check_rows(c, "q", p->q, p->q_stride, d.qdim()));
+  AE_TRY(check_rows(c, "out", p->out, p->out_stride, d.qdim()));
+  AE_TRY(check_rows(c, "k", p->k, p->kv_stride, d.kvdim()));
+  AE_TRY(check_rows(c, "v", p->v, p->kv_stride, d.kvdim()));
+  AE_TRY(check_device(c));
+  a.batch = p->batch;
+  a.causal = p->causal != 0;
+  a.Hq = d.Hq;
+  a.Hkv = d.Hkv;
+  a.cache_rows = p->cache_rows;
+  a.q = (const ae::bf16*)p->q;
+  a.k = (const ae::bf16*)p->k;
+  a.v = (const ae::bf16*)p->v;
+  a.q_stride = p->q_stride;
+  a.kv_stride = p->kv_stride;
+  a.out_stride = p->out_stride;
+  a.key_mask = p->key_mask;
+  a.scale = p->scale > 0.f ? p->scale : (float)(1.0 / sqrt((double)d.dh));
+  a.out = (ae::bf16*)p->out;
+  a.status = c->status_dev;
+  return launched(c, ae::launch_prompt_attention(a, d.dh, c->sm_count, c->stream), op);
+}
+
+ae_status ae_token_attention(ae_ctx* c, const ae_token_attention_args* p) {
+  if (c == nullptr) return AE_ERR_INVALID_ARG;
+  const char* op = "ae_token_attention";
+  AE_TRY(check_context(c, p, op));
+  const ae::Dims& d = c->d;
+  if (p->batch < 0 || p->batch > AE_MAX_TOKENS)
+    return fail(c, AE_ERR_SHAPE, "batch %d outside 0..%d", p->batch, AE_MAX_TOKENS);
+  if (p->max_len < 0) return fail(c, AE_ERR_SHAPE, "max_len %d < 0", p->max_len);
+  AE_TRY(check_scale(c, p->scale));
+  AE_TRY(check_cache_rows(c, p->cache_rows));
+  if (p->batch == 0) return AE_OK;
+  if (p->kv_row0 == nullptr || p->kv_len == nullptr)
+    return fail(c, AE_ERR_INVALID_ARG, "kv_row0 / kv_len is NULL");
+  if ((uintptr_t)p->kv_row0 % 8 != 0 || (uintptr_t)p->kv_len % 4 != 0)
+    return fail(c, AE_ERR_INVALID_ARG, "kv_row0 / kv_len is not aligned to its elements");
+  AE_TRY(check_rows(c, "q", p->q, p->q_stride, d.qdim()));
+  AE_TRY(check_rows(c, "out", p->out, p->out_stride, d.qdim()));
+  if (p->cache_rows > 0) {
+    AE_TRY(check_rows(c, "k", p->k, p->kv_stride, d.kvdim()));
+    AE_TRY(check_rows(c, "v", p->v, p->kv_stride, d.kvdim()));
+  }
+  AE_TRY(check_device(c));
+  ae::TokenAttnArgs a;
+  a.batch = p->batch;
+  a.max_len = p->max_len;
+  a.Hq = d.Hq;
+  a.Hkv = d.Hkv;
+  a.kv_row0 = p->kv_row0;
+  a.kv_len = p->kv_len;
+  a.cache_rows = p->cache_rows;
+  a.q = (const ae::bf16*)p->q;
+  a.k = (const ae::bf16*)p->k;
+  a.v = (const ae::bf16*)p->v;
+  a.q_stride = p->q_stride;
+  a.kv_stride = p->kv_stride;
+  a.out_stride = p->out_stride;
+  a.key_mask = p->key_mask;
+  a.scale = p->scale > 0.f ? p->scale : (float)(1.0 / sqrt((double)d.dh));
+  a.out = (ae::bf16*)p->out;
+  a.status = c->status_dev;
+  return launched(c, ae::launch_token_attention(a, d.dh, c->sm_count, c->stream), op);
+}
+
+}  // extern "C"

@@ -251,6 +251,128 @@ AE_API ae_status ae_bind_context(ae_ctx* ctx, int batch, const void* hidden, con
  */
 AE_API ae_status ae_prefill(ae_ctx* ctx, int batch, const void* embeddings, void* out_k, void* out_v);
 
+/* ---- Operators of a language-model attention layer -------------------------
+ *
+ * What a decoder layer's attention needs around its Linears, on the context's
+ * head layout (n_q_heads, n_kv_heads, head_dim), rms_eps, rope_theta and
+ * stream: per-head norms with the rotation into a K/V cache, attention of
+ * packed prompts, attention of single new tokens over the cache (MolmoBot PR,
+ * Part 2: a 4B decoder is the VLM backbone; OxyGen: language requests decode
+ * over the same KV the action expert reads).  ae_prefill_prompts runs the
+ * context's layers with the first two.
+ *
+ * Common to the operators:
+ *   - bf16 contexts only (AE_ERR_UNSUPPORTED otherwise), called while the
+ *     context's device is current (AE_ERR_INVALID_ARG otherwise).  They use
+ *     none of the context's scratch and no workspace, allocate nothing, and
+ *     may be captured into a CUDA graph: calls of one context on different
+ *     streams (ae_set_stream between them) and replays of several graphs may
+ *     overlap as long as their outputs do not.  Host arrays are read before
+ *     the call returns (a captured graph keeps the values of the capture).
+ *   - A row stride is in elements, at least the row's length and a multiple of
+ *     8; every bf16 pointer is 16-byte aligned (AE_ERR_INVALID_ARG otherwise).
+ *     Row indices times strides may exceed 32 bits.
+ *   - Elements of a row beyond its heads, rows no sequence or token names, and
+ *     cache rows not written are left as they were.
+ *   - Outputs do not depend on the other sequences or tokens of a call except
+ *     through the split of long key ranges (ae_prompt_attention,
+ *     ae_token_attention), which changes the order of fp32 sums.  Every call
+ *     with the same arguments gives the same bits.
+ */
+
+/*
+ * Per-head RMS norm of queries and keys, rotary positions on one or several
+ * axes, and the write of keys and values into a cache, in one pass over the
+ * merged projection.  For token t and a query or key head x[0 .. dh-1]:
+ *   y[i]          = x[i] / sqrt(mean(x^2) + rms_eps) * (norm_offset + w[i])
+ *   phi(j)        = positions[pair_axis[j]][t] * pair_freq[j],   j < dh/2
+ *   out[j]        = y[j] cos phi - y[j + dh/2] sin phi
+ *   out[j + dh/2] = y[j + dh/2] cos phi + y[j] sin phi
+ * in fp32, rounded once to bf16 (the angle is reduced exactly: every int32
+ * position is as accurate as small ones).  Values are copied.
+ */
+typedef struct {
+  int tokens;                /* >= 0                                             */
+  int n_axes;                /* rows of positions, 1..AE_MAX_AXES                */
+  const void* qkv;           /* device bf16 [tokens][q heads | k heads | v heads] */
+  int64_t qkv_stride;
+  const void *q_norm, *k_norm; /* device bf16 [dh] norm weights; NULL: no norm   */
+  float norm_offset;         /* 0: multiply by w; 1: by 1 + w                    */
+  const int32_t* positions;  /* device [n_axes][tokens]                          */
+  const uint8_t* pair_axis;  /* HOST [dh/2], axis of every rotation pair, < n_axes; NULL: all axis 0 */
+  const double* pair_freq;   /* HOST [dh/2], radians per position, finite (0: the pair is not rotated);
+                                NULL: rope_theta^(-2j/dh)                        */
+  const int64_t* kv_rows;    /* device [tokens], cache row of every token, distinct; negative: the token's
+                                K and V are not stored; >= cache_rows: not stored, and the context's status
+                                becomes AE_ERR_DEVICE.  NULL: token t goes to row t */
+  int64_t cache_rows;        /* rows of k_cache / v_cache (>= tokens without kv_rows) */
+  void* q_out;               /* device bf16 [tokens][Hq dh]; may be qkv with q_stride == qkv_stride (in place) */
+  int64_t q_stride;
+  void *k_cache, *v_cache;   /* device bf16 [cache_rows][Hkv dh], no overlap with qkv or q_out */
+  int64_t kv_stride;
+} ae_qk_norm_rope_args;
+#define AE_MAX_AXES 4
+AE_API ae_status ae_qk_norm_rope(ae_ctx* ctx, const ae_qk_norm_rope_args* args);
+
+/*
+ * Attention of packed prompts: sequence b owns query rows cu_q[b] ..
+ * cu_q[b+1]-1 and attends to kv_len[b] cache rows from kv_row0[b], of which its
+ * own tokens are the last ones (kv_len[b] >= its query count; more is a cached
+ * beginning the prompt continues).  Query i of sequence b sees keys
+ * 0 .. kv_len[b] - n_b + i (causal) or all of them (causal == 0), without the
+ * masked ones:
+ *   out = sum_j softmax_j(scale q . k_j) v_j      fp32, rounded to bf16
+ * with the softmax weights rounded to bf16 before they meet v; 0 where no key
+ * is left.  Query head h reads KV head h / (n_q_heads / n_kv_heads).  Masked
+ * rows may hold anything (NaN included), rows outside the sequences too; the
+ * unmasked rows of a sequence must be finite (a non-finite value row may reach
+ * every query of its sequence).
+ */
+typedef struct {
+  int batch;                 /* sequences, 0..AE_MAX_BATCH                       */
+  int causal;
+  const int32_t* cu_q;       /* HOST [batch + 1], cu_q[0] == 0, non-decreasing   */
+  const int64_t* kv_row0;    /* HOST [batch] or NULL with kv_len: the keys are packed as the queries */
+  const int32_t* kv_len;     /* HOST [batch] or NULL with kv_row0                */
+  int64_t cache_rows;        /* rows of k / v / key_mask                         */
+  const void* q;             /* device bf16 [cu_q[batch]][Hq dh]                 */
+  int64_t q_stride;
+  const void *k, *v;         /* device bf16 [cache_rows][Hkv dh]                 */
+  int64_t kv_stride;
+  const uint8_t* key_mask;   /* device [cache_rows], 0 = masked; NULL: none      */
+  float scale;               /* 0: 1 / sqrt(dh)                                  */
+  void* out;                 /* device bf16 [cu_q[batch]][Hq dh]                 */
+  int64_t out_stride;
+} ae_prompt_attention_args;
+AE_API ae_status ae_prompt_attention(ae_ctx* ctx, const ae_prompt_attention_args* args);
+
+/*
+ * Attention of one new token per request over its cached rows: request b's
+ * query sees cache rows kv_row0[b] .. kv_row0[b] + kv_len[b] - 1 without the
+ * masked ones, all of them (the new token's own K and V are already stored).
+ * Lengths and first rows are read on the device, so a captured graph follows
+ * them as they grow.  Formula, mask, finiteness and empty rows as in
+ * ae_prompt_attention.  A length above max_len, or a range outside the cache,
+ * is cut to what is inside and the context's status becomes AE_ERR_DEVICE.
+ */
+typedef struct {
+  int batch;                 /* requests, 0..AE_MAX_TOKENS                       */
+  int max_len;               /* no kv_len is larger; sets the split of the work  */
+  const int64_t* kv_row0;    /* device [batch]                                   */
+  const int32_t* kv_len;     /* device [batch], 0: the output row is 0           */
+  int64_t cache_rows;
+  const void* q;             /* device bf16 [batch][Hq dh]                       */
+  int64_t q_stride;
+  const void *k, *v;         /* device bf16 [cache_rows][Hkv dh]                 */
+  int64_t kv_stride;
+  const uint8_t* key_mask;   /* device [cache_rows] or NULL                      */
+  float scale;
+  void* out;                 /* device bf16 [batch][Hq dh]                       */
+  int64_t out_stride;
+} ae_token_attention_args;
+#define AE_MAX_TOKENS 65535
+AE_API ae_status ae_token_attention(ae_ctx* ctx, const ae_token_attention_args* args);
+
 /*
  * Run n_steps Euler steps of delta = -1/n_steps from t = 1 for every bound
  * request (MolmoBot Part 2), the velocity of step k taken at t = 1 - k/n_steps.
