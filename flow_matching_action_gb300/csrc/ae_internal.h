@@ -333,6 +333,9 @@ cudaError_t launch_attn_tc(const CUtensorMap& qmap, const CUtensorMap& kmap, con
                            const CUtensorMap& omap, const CUtensorMap* omap16, AttnArgs a, bf16* o, int sm_count,
                            cudaStream_t s, bool pdl);
 cudaError_t make_bf16_map(CUtensorMap* map, const void* ptr, long rows, long cols, int box_rows);
+// bf16 [dim2][dim1][dim0] view, strides of dims 1 and 2 in elements, 128-byte swizzle
+cudaError_t make_bf16_3d_map(CUtensorMap* map, const void* ptr, const long (&dim)[3], const long (&stride)[2],
+                             const int (&box)[3]);
 // fp32 [d2][d1][d0] view with boxes {32, box1, 1}, 128-byte swizzle (split-K partials)
 cudaError_t make_kv3d_map(CUtensorMap* map, const void* ptr, long rows, long kvdim, int dh);
 cudaError_t make_f32_3d_map(CUtensorMap* map, const void* ptr, long d0, long d1, long d2, int box1);
@@ -377,6 +380,7 @@ struct PromptAttnArgs {
   int64_t kv_row0[AE_MAX_BATCH];
 };
 cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int dh, int sm_count, cudaStream_t s);
+cudaError_t prompt_kernel_setup();
 
 struct TokenAttnArgs {
   int batch, max_len, Hq, Hkv;

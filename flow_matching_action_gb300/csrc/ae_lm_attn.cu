@@ -1,4 +1,4 @@
-// Attention of packed prompts and of single tokens, first form: one warp per
+// Attention of single tokens, first form: one warp per
 // (query row, head) walks the row's keys with a running maximum and sum; a
 // lane holds DH / 32 consecutive dims of q, k, v and o.
 #include <math.h>
@@ -48,20 +48,6 @@ __device__ void attend_row(const bf16* q, const bf16* k, const bf16* v, int64_t 
 }
 
 template <int DH>
-__global__ void k_prompt_rows(const __grid_constant__ PromptAttnArgs a) {
-  const int row = blockIdx.x, h = blockIdx.y * 4 + (threadIdx.x >> 5);
-  if (h >= a.Hq) return;
-  int b = 0;
-  while (row >= a.cu_q[b + 1]) ++b;
-  const int n_new = a.cu_q[b + 1] - a.cu_q[b];
-  const int n_keys = a.causal ? a.kv_len[b] - n_new + (row - a.cu_q[b]) + 1 : a.kv_len[b];
-  const int64_t r0 = a.kv_row0[b], col = (int64_t)(h / (a.Hq / a.Hkv)) * DH;
-  attend_row<DH>(a.q + row * a.q_stride + (int64_t)h * DH, a.k + r0 * a.kv_stride + col, a.v + r0 * a.kv_stride + col,
-                 a.kv_stride, a.key_mask ? a.key_mask + r0 : nullptr, n_keys, a.scale,
-                 a.out + row * a.out_stride + (int64_t)h * DH);
-}
-
-template <int DH>
 __global__ void k_token_rows(const __grid_constant__ TokenAttnArgs a) {
   const int b = blockIdx.x, h = blockIdx.y * 4 + (threadIdx.x >> 5);
   if (h >= a.Hq) return;
@@ -83,14 +69,6 @@ __global__ void k_token_rows(const __grid_constant__ TokenAttnArgs a) {
 
 }  // namespace
 
-cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int dh, int sm_count, cudaStream_t s) {
-  (void)sm_count;
-  const dim3 grid(a.cu_q[a.batch], (a.Hq + 3) / 4);
-  if (dh == 64) return launch_k(k_prompt_rows<64>, grid, dim3(128), 0, s, false, a);
-  if (dh == 128) return launch_k(k_prompt_rows<128>, grid, dim3(128), 0, s, false, a);
-  return launch_k(k_prompt_rows<256>, grid, dim3(128), 0, s, false, a);
-}
-
 cudaError_t launch_token_attention(const TokenAttnArgs& a, int dh, int sm_count, cudaStream_t s) {
   (void)sm_count;
   const dim3 grid(a.batch, (a.Hq + 3) / 4);
@@ -99,6 +77,6 @@ cudaError_t launch_token_attention(const TokenAttnArgs& a, int dh, int sm_count,
   return launch_k(k_token_rows<256>, grid, dim3(128), 0, s, false, a);
 }
 
-cudaError_t lm_kernel_setup() { return cudaSuccess; }
+cudaError_t lm_kernel_setup() { return prompt_kernel_setup(); }
 
 }  // namespace ae

@@ -1,0 +1,683 @@
+// Attention of packed prompts on the tensor cores (ae_prompt_attention).
+//
+// The query heads of a KV group are folded into the rows of a tile: a tile is
+// T = 128 / G consecutive tokens of a sequence times its G heads (row =
+// token * G + head; T * G <= 128 rows used), so short prompts fill tiles and a
+// causal diagonal covers few keys.  One CTA works on NQ tiles of one
+// (sequence, KV head) and walks the keys in tiles of BK with an online softmax:
+//   S = Q K^T     tcgen05, M = 128, N = BK, fp32 in tensor memory
+//   P = 2^(c S - m) one thread per row; bf16 back over the S columns it read
+//   O += P V      tcgen05, P as the TMEM A operand, O stays in tensor memory
+// The exponent reference m is raised (and O, l rescaled) only when a row's
+// maximum passes it by more than 2^8, so most tiles skip the rescale and P is
+// at most 2^8; l sums the fp32 weights, P is rounded to bf16 for the tensor
+// cores.
+// Roles: one warpgroup per tile does the softmax, one warp issues TMA loads
+// into a ring of K and V tiles, one warp issues the MMAs.
+//   NQ = 2 (head_dim 64, 128): the two tiles alternate, one tile's MMAs run
+//           under the other's softmax.
+//   NQ = 1 (head_dim 256, whose O fills half of tensor memory): two S buffers,
+//           the next tile's Q K^T runs under this tile's softmax.
+// Keys that a row may not see get score -inf; V rows that no row may see (a
+// sequence's end inside the tile, masked rows) are zeroed in shared memory,
+// since 0 * NaN would reach every row.
+// Few query rows over many keys leave SMs idle: the key tiles are then split
+// over the CTAs of a cluster, which exchange fp32 partials through distributed
+// shared memory (no workspace, one launch, sums in rank order).
+#include <math.h>
+
+#include "ae_internal.h"
+#include "ae_tc.cuh"
+
+namespace ae {
+namespace {
+
+using namespace tc;
+
+constexpr float kRaise = 8.f;  // log2: raise the exponent reference past this
+
+template <int DH>
+struct Cfg {
+  static constexpr int NQ = DH == 256 ? 1 : 2;
+  static constexpr int BK = DH == 256 ? 64 : 128;
+  static constexpr int DB = DH / 64;               // 64-dim blocks of a row
+  static constexpr int SLOT = BK * DH * 2;         // bytes of a K or V tile
+  static constexpr int NS = DH == 64 ? 8 : 5;      // ring slots
+  static constexpr int QBYTES = 128 * DH * 2;      // bytes of a query tile
+  static constexpr int THREADS = NQ * 128 + 64;
+  static constexpr int W_LOAD = NQ * 4, W_MMA = NQ * 4 + 1;
+  // shared memory, from a 1024-byte boundary
+  static constexpr int RING = NQ * QBYTES;
+  static constexpr int BARS = RING + NS * SLOT;
+  static constexpr int ML = NQ * 128 * DH * 4;     // a split's partial: fp32 rows, then [NQ][128] (m, l)
+  static constexpr int BYTES = BARS + 256 + 1024;
+  // tensor memory columns
+  static constexpr int O0 = 256;
+  static_assert(ML + NQ * 128 * 8 <= BARS, "fp32 partials fit over the tiles");
+  static_assert(BYTES <= 227 * 1024, "shared memory");
+};
+
+struct Launch {
+  int n_order;                       // sequences with work
+  int G, Gc, hc, T;                  // heads of a group, of a tile; head chunks; tokens of a tile
+  int split;                         // CTAs of a cluster
+  int work_cu[AE_MAX_BATCH + 1];     // first work unit of the i-th sequence, longest first
+  uint8_t order[AE_MAX_BATCH];
+};
+
+struct Bars {
+  uint64_t q, full[8], empty[8], s[2], p[2], o[2], drain;
+  uint32_t tmem;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 256, "");
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+#define AE_R8(r, o) "=r"(r[o]), "=r"(r[o + 1]), "=r"(r[o + 2]), "=r"(r[o + 3]), "=r"(r[o + 4]), "=r"(r[o + 5]), \
+                    "=r"(r[o + 6]), "=r"(r[o + 7])
+#define AE_U8(r, o) "+r"(r[o]), "+r"(r[o + 1]), "+r"(r[o + 2]), "+r"(r[o + 3]), "+r"(r[o + 4]), "+r"(r[o + 5]), \
+                    "+r"(r[o + 6]), "+r"(r[o + 7])
+#define AE_I8(r, o) "r"(r[o]), "r"(r[o + 1]), "r"(r[o + 2]), "r"(r[o + 3]), "r"(r[o + 4]), "r"(r[o + 5]), \
+                    "r"(r[o + 6]), "r"(r[o + 7])
+
+// Start of a load of 32 lanes x 32 columns; the registers hold the values only
+// after tmem_ld_wait() and landed().
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : AE_R8(r, 0), AE_R8(r, 8), AE_R8(r, 16), AE_R8(r, 24)
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Orders uses of r behind the wait before it (the wait does not name the registers).
+__device__ __forceinline__ void landed(uint32_t (&r)[32]) {
+  asm volatile("" : AE_U8(r, 0), AE_U8(r, 8), AE_U8(r, 16), AE_U8(r, 24));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(
+          taddr),
+      AE_I8(r, 0), AE_I8(r, 8), AE_I8(r, 16), AE_I8(r, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// mbar_wait of a whole warp: one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort, int* status) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, status));
+}
+
+// First n bits of the k-th word.
+__device__ __forceinline__ uint32_t low_bits(int n, int k) {
+  n -= 32 * k;
+  return n <= 0 ? 0u : (n >= 32 ? 0xffffffffu : (1u << n) - 1u);
+}
+
+// Valid keys of the tile at key0 of a sequence of n_keys keys (bit = key;
+// mask: the sequence's mask bytes or nullptr).  Whole warp.
+template <int BK>
+__device__ __forceinline__ void tile_bits(const uint8_t* mask, int key0, int n_keys, uint32_t (&w)[BK / 32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int k = 0; k < BK / 32; ++k) {
+    if (mask != nullptr) {
+      const int key = key0 + 32 * k + lane;
+      w[k] = __ballot_sync(0xffffffffu, key < n_keys && mask[key] != 0);
+    } else {
+      w[k] = low_bits(n_keys - key0, k);
+    }
+  }
+}
+
+// A work unit: NQ tiles of one (sequence, KV head, chunk of its heads), and
+// this CTA's range [lo, hi) of key tiles.
+struct Unit {
+  int tok0;        // first token of the first tile, within its sequence
+  int n_new, n_keys, q_row0;
+  int64_t kv_row0;
+  int kvh, g0;     // KV head; first head of the tile within its group
+};
+
+template <int DH>
+__device__ __forceinline__ Unit find_unit(const PromptAttnArgs& a, const Launch& L, int u) {
+  int i = 0;
+#pragma unroll
+  for (int step = 32; step > 0; step >>= 1)
+    if (i + step < L.n_order && L.work_cu[i + step] <= u) i += step;
+  const int b = L.order[i];
+  u -= L.work_cu[i];
+  Unit w;
+  w.q_row0 = a.cu_q[b];
+  w.n_new = a.cu_q[b + 1] - a.cu_q[b];
+  w.n_keys = a.kv_len[b];
+  w.kv_row0 = a.kv_row0[b];
+  const int per = a.Hkv * L.hc;
+  const int tiles = (w.n_new + L.T * Cfg<DH>::NQ - 1) / (L.T * Cfg<DH>::NQ);
+  const int t = tiles - 1 - u / per;  // longest key ranges first
+  const int h = u % per;
+  w.kvh = h / L.hc;
+  w.g0 = (h - w.kvh * L.hc) * L.Gc;
+  w.tok0 = t * L.T * Cfg<DH>::NQ;
+  return w;
+}
+
+template <int DH>
+__global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
+    k_prompt_attn(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PromptAttnArgs a,
+                  const __grid_constant__ Launch L) {
+  using C = Cfg<DH>;
+  constexpr int NQ = C::NQ, BK = C::BK, DB = C::DB, NS = C::NS;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Bars* B = reinterpret_cast<Bars*>(smem + C::BARS);
+  volatile int* abort_flag = &B->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = L.split > 1 ? (int)cluster_rank() : 0;
+  const Unit w = find_unit<DH>(a, L, blockIdx.x / L.split);
+  const uint8_t* mask = a.key_mask ? a.key_mask + w.kv_row0 : nullptr;
+
+  // key tiles of every query tile: up to its last token's last key
+  int cnt[NQ], most = 0;
+#pragma unroll
+  for (int s = 0; s < NQ; ++s) {
+    const int t0 = w.tok0 + s * L.T;
+    const int last = min(t0 + L.T, w.n_new) - 1;
+    const int keys = t0 >= w.n_new ? 0 : (a.causal ? w.n_keys - w.n_new + last + 1 : w.n_keys);
+    cnt[s] = (keys + BK - 1) / BK;
+    most = max(most, cnt[s]);
+  }
+  const int lo = (int)((int64_t)most * rank / L.split), hi = (int)((int64_t)most * (rank + 1) / L.split);
+  int n_tiles = 0;
+#pragma unroll
+  for (int s = 0; s < NQ; ++s) {
+    cnt[s] = max(0, min(cnt[s], hi) - lo);
+    n_tiles = max(n_tiles, cnt[s]);
+  }
+
+  if (threadIdx.x == 0) {
+    mbar_init(&B->q, 1);
+    mbar_init(&B->drain, 1);
+    for (int i = 0; i < 8; ++i) {
+      mbar_init(&B->full[i], 1);
+      mbar_init(&B->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B->s[i], 1);
+      mbar_init(&B->p[i], 4);
+      mbar_init(&B->o[i], 1);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::W_MMA) {
+    tmem_alloc(&B->tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B->tmem;
+
+  if (warp == C::W_LOAD) {
+    // ---------------------------------------------------------------- loads
+    if (lane == 0 && n_tiles > 0) {
+      mbar_arrive_expect_tx(&B->q, (uint32_t)(NQ * DB * L.T * L.Gc * 128));
+#pragma unroll
+      for (int s = 0; s < NQ; ++s)
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+          tma_load_3d_nohint(smem + s * C::QBYTES + d * (128 * 128), &qmap, &B->q, d * 64,
+                             w.kvh * L.G + w.g0, w.q_row0 + w.tok0 + s * L.T);
+      int c = 0;
+      bool ok = true;
+      auto load = [&](const CUtensorMap* map, int t) {
+        const int slot = c % NS;
+        if (c >= NS) ok = mbar_wait(&B->empty[slot], (uint32_t)((c / NS) & 1) ^ 1u, abort_flag, a.status);
+        if (!ok) return;
+        mbar_arrive_expect_tx(&B->full[slot], C::SLOT);
+        tma_load_3d_nohint(smem + C::RING + slot * C::SLOT, map, &B->full[slot], 0,
+                           (int)(w.kv_row0 + (int64_t)t * BK), w.kvh * DB);
+        ++c;
+      };
+      if (NQ == 1) load(&kmap, lo);
+      for (int i = 0; i < n_tiles && ok; ++i) {
+        if (NQ == 2) load(&kmap, lo + i);
+        else if (i + 1 < n_tiles) load(&kmap, lo + i + 1);
+        if (ok) load(&vmap, lo + i);
+      }
+      // every copy lands before the CTA's shared memory is released, also after a failure
+      mbar_drain(&B->q, 0, a.status);
+      for (int i = max(0, c - NS); i < c; ++i) mbar_drain(&B->full[i % NS], (uint32_t)(i / NS) & 1u, a.status);
+    }
+  } else if (warp == C::W_MMA) {
+    // ---------------------------------------------------------------- MMAs
+    constexpr uint32_t idesc_s = idesc_bf16(128, BK), idesc_o = idesc_bf16(128, DH, true);
+    int c = 0;  // ring slots consumed
+    bool ok = n_tiles == 0 || warp_wait(&B->q, 0, abort_flag, a.status);
+    auto wait_slot = [&](int i) { return warp_wait(&B->full[i % NS], (uint32_t)(i / NS) & 1u, abort_flag, a.status); };
+    auto qk = [&](int s, int buf, int slot) {
+      if (lane == 0) {
+#pragma unroll
+        for (int d = 0; d < DB; ++d) {
+          const uint64_t ad = sdesc_sw128(smem_u32(smem + s * C::QBYTES + d * (128 * 128)));
+          const uint64_t bd = sdesc_sw128(smem_u32(smem + C::RING + slot * C::SLOT + d * (BK * 128)));
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_bf16(tmem + (uint32_t)(buf * BK), ad + 2 * k, bd + 2 * k, idesc_s, (d > 0 || k > 0) ? 1u : 0u);
+        }
+        mma_commit(&B->s[buf]);
+      }
+    };
+    auto pv = [&](int s, int buf, int slot, bool first) {
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < BK / 16; ++k) {
+          const uint64_t bd = sdesc_sw128_mn(smem_u32(smem + C::RING + slot * C::SLOT + k * 2048), BK * 128, 1024);
+          mma_bf16_ts(tmem + (uint32_t)(C::O0 + s * DH), tmem + (uint32_t)(buf * BK + 8 * k), bd, idesc_o,
+                      (!first || k > 0) ? 1u : 0u);
+        }
+      }
+    };
+    auto release = [&](int slot) {
+      if (lane == 0) mma_commit(&B->empty[slot]);
+    };
+    // zero the V rows of tile i that no query may see
+    auto clean_v = [&](int i, int slot) {
+      const int key0 = (lo + i) * BK;
+      if (mask == nullptr && key0 + BK <= w.n_keys) return;
+      uint32_t bits[BK / 32];
+      tile_bits<BK>(mask, key0, w.n_keys, bits);
+      uint32_t all = 0xffffffffu;
+#pragma unroll
+      for (int k = 0; k < BK / 32; ++k) all &= bits[k];
+      if (all == 0xffffffffu) return;
+      uint8_t* v = smem + C::RING + slot * C::SLOT;
+#pragma unroll
+      for (int k = 0; k < BK / 32; ++k)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          // 16-byte piece lane + 32 e of this word's 32 rows: row (lane + 32 e) / 8
+          const int r = (lane >> 3) + 4 * e;
+          if (!((bits[k] >> r) & 1u))
+#pragma unroll
+            for (int d = 0; d < DB; ++d)
+              *reinterpret_cast<uint4*>(v + d * (BK * 128) + (32 * k + r) * 128 + (lane & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+        }
+      fence_proxy_async_smem();
+      __syncwarp();
+    };
+    if (NQ == 2) {
+      if (n_tiles > 0 && ok && (ok = wait_slot(0))) {
+#pragma unroll
+        for (int s = 0; s < NQ; ++s)
+          if (cnt[s] > 0) qk(s, s, 0);
+        release(0);
+        c = 1;
+      }
+      for (int i = 0; i < n_tiles && ok; ++i) {
+        // slot c: V of tile i, slot c + 1: K of tile i + 1
+        if (!(ok = wait_slot(c))) break;
+        clean_v(i, c % NS);
+        bool have_k = false;
+#pragma unroll
+        for (int s = 0; s < NQ; ++s) {
+          if (ok && i < cnt[s]) {
+            if (!(ok = warp_wait(&B->p[s], (uint32_t)i & 1u, abort_flag, a.status))) break;
+            tc_fence_after();
+            pv(s, s, c % NS, i == 0);
+            if (i + 1 == cnt[s] && lane == 0) mma_commit(&B->o[s]);
+          }
+          if (ok && i + 1 < cnt[s]) {
+            if (!have_k && !(ok = wait_slot(c + 1))) break;
+            have_k = true;
+            qk(s, s, (c + 1) % NS);
+          }
+        }
+        if (!ok) break;
+        release(c % NS);
+        if (i + 1 < n_tiles) release((c + 1) % NS);
+        c += 2;
+      }
+    } else {
+      if (n_tiles > 0 && ok && (ok = wait_slot(0))) {
+        qk(0, 0, 0);
+        release(0);
+        c = 1;
+      }
+      for (int i = 0; i < n_tiles && ok; ++i) {
+        if (i + 1 < n_tiles) {
+          if (!(ok = wait_slot(c))) break;
+          qk(0, (i + 1) & 1, c % NS);
+          release(c % NS);
+          ++c;
+        }
+        if (!(ok = wait_slot(c))) break;
+        clean_v(i, c % NS);
+        if (!(ok = warp_wait(&B->p[i & 1], (uint32_t)(i >> 1) & 1u, abort_flag, a.status))) break;
+        tc_fence_after();
+        pv(0, i & 1, c % NS, i == 0);
+        if (lane == 0) mma_commit(&B->o[i & 1]);
+        release(c % NS);
+        ++c;
+      }
+    }
+    if (!ok && lane == 0) {  // MMAs in flight must finish before tensor memory is freed
+      mma_commit(&B->drain);
+      mbar_drain(&B->drain, 0, a.status);
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- softmax
+    const int s = warp >> 2;             // query tile of this warpgroup
+    const int row = threadIdx.x & 127;   // its row, the TMEM lane
+    const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
+    const int tok = row / L.Gc, g = w.g0 + row - tok * L.Gc;
+    const int t0 = w.tok0 + s * L.T;
+    const bool real = tok < L.T && t0 + tok < w.n_new && g < L.G;
+    // keys this row sees; keys every row of the tile sees
+    const int back = a.causal ? w.n_keys - w.n_new + 1 : 0;
+    const int limit = !real ? 0 : (a.causal ? back + t0 + tok : w.n_keys);
+    const int open = a.causal ? back + t0 : w.n_keys;
+    const float c = a.scale * 1.4426950408889634f;  // scores in the log2 domain
+    const uint32_t tm_o = tmem + lane_off + (uint32_t)(C::O0 + s * DH);
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    const int n = cnt[NQ == 1 ? 0 : s];
+    for (int i = 0; i < n; ++i) {
+      const int buf = NQ == 1 ? i & 1 : s;
+      const uint32_t tm_s = tmem + lane_off + (uint32_t)(buf * BK);
+      const int key0 = (lo + i) * BK;
+      const bool partial = mask != nullptr || key0 + BK > open;
+      uint32_t bits[BK / 32];
+      if (partial) {
+        tile_bits<BK>(mask, key0, w.n_keys, bits);
+#pragma unroll
+        for (int k = 0; k < BK / 32; ++k) bits[k] &= low_bits(limit - key0, k);
+      }
+      if (!warp_wait(&B->s[buf], (uint32_t)(NQ == 1 ? i >> 1 : i) & 1u, abort_flag, a.status)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      uint32_t sc[BK / 32][32];
+#pragma unroll
+      for (int k = 0; k < BK / 32; ++k) tmem_ld32_start(tm_s + 32 * k, sc[k]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < BK / 32; ++k) landed(sc[k]);
+      if (partial) {
+#pragma unroll
+        for (int k = 0; k < BK / 32; ++k)
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if (!((bits[k] >> j) & 1u)) sc[k][j] = 0xff800000u;  // -inf
+      }
+      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int k = 0; k < BK / 32; ++k)
+#pragma unroll
+        for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sc[k][j]));
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+      float factor = 1.f;
+      if (top > m + kRaise) {  // -inf stays -inf while no key has been seen
+        factor = ex2_fast(m - top);
+        m = top;
+      }
+      if (i > 0 && __any_sync(0xffffffffu, factor != 1.f)) {
+        // O holds tiles 0 .. i-1: with NQ = 2 their P V are done (S of this
+        // tile was issued behind them), with NQ = 1 the last one may still run
+        if (NQ == 1 && !warp_wait(&B->o[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, abort_flag, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        l *= factor;
+#pragma unroll 1
+        for (int d = 0; d < DH; d += 32) {
+          uint32_t o[32];
+          tmem_ld32_start(tm_o + d, o);
+          tmem_ld_wait();
+          landed(o);
+#pragma unroll
+          for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * factor);
+          tmem_st32(tm_o + d, o);
+        }
+        tmem_st_wait();
+      }
+      const float base = m == -INFINITY ? 0.f : -m;
+      const uint64_t c2 = pack2(c, c), b2 = pack2(base, base);
+      uint64_t sum[2] = {0, 0};
+#pragma unroll
+      for (int h = 0; h < BK / 64; ++h) {
+        uint32_t p[32];
+#pragma unroll
+        for (int j = 0; j < 64; j += 2) {
+          const int k = 2 * h + (j >> 5), e = j & 31;
+          float x, y;
+          unpack2(fma2(pack2(__uint_as_float(sc[k][e]), __uint_as_float(sc[k][e + 1])), c2, b2), x, y);
+          x = ex2_fast(x);
+          y = ex2_fast(y);
+          sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pack2(x, y));
+          p[j >> 1] = bf16x2(x, y);
+        }
+        tmem_st32(tm_s + 32 * h, p);  // over S columns read above
+      }
+      float x, y;
+      unpack2(add2(sum[0], sum[1]), x, y);
+      l += x + y;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B->p[buf]);
+    }
+    if (ok && n > 0)
+      ok = NQ == 1 ? warp_wait(&B->o[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u, abort_flag, a.status)
+                   : warp_wait(&B->o[s], 0, abort_flag, a.status);
+    __syncwarp();
+    tc_fence_after();
+    if (ok && L.split == 1) {
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      bf16* dst = a.out + (int64_t)(w.q_row0 + t0 + tok) * a.out_stride + (int64_t)(w.kvh * L.G + g) * DH;
+#pragma unroll 1
+      for (int d = 0; d < DH; d += 32) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld32_start(tm_o + d, o);
+          tmem_ld_wait();
+          landed(o);
+        }
+        if (real) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              v[e] = l > 0.f ? bf16x2(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv)
+                             : 0u;
+            *reinterpret_cast<uint4*>(dst + d + 8 * q) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+    } else if (L.split > 1) {
+      // this split's partial into shared memory, over the tiles: every TMA copy
+      // and MMA of both warpgroups' tiles must have finished reading them
+      if (NQ == 2) asm volatile("bar.sync 1, 256;" ::: "memory");
+      reinterpret_cast<float2*>(smem + C::ML)[s * 128 + row] = ok ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
+      uint8_t* part = smem + (s * 128 + row) * (DH * 4);
+#pragma unroll 1
+      for (int d = 0; d < DH; d += 32) {
+        uint32_t o[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] = 0u;
+        if (n > 0 && ok) {
+          tmem_ld32_start(tm_o + d, o);
+          tmem_ld_wait();
+          landed(o);
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)  // 16-byte pieces XORed by row: conflict-free
+          *reinterpret_cast<uint4*>(part + ((((d >> 2) + q) ^ (row & 7)) << 4)) =
+              make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::W_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+  if (L.split > 1) {
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    // rank r merges its share of the rows, DH / 4 lanes-of-four per row
+    const int rows = NQ * 128, share = rows / L.split;
+    constexpr int PER = DH / 4;
+    const uint32_t base = smem_u32(smem), ml = smem_u32(smem + C::ML);
+    for (int i = threadIdx.x; i < share * PER; i += C::THREADS) {
+      const int r = rank * share + i / PER, q = i % PER;
+      const int s = r >> 7, rr = r & 127;
+      const int tok = rr / L.Gc, g = w.g0 + rr - tok * L.Gc;
+      const int t = w.tok0 + s * L.T + tok;
+      if (tok >= L.T || t >= w.n_new || g >= L.G) continue;
+      float m = -INFINITY;
+      for (int p = 0; p < L.split; ++p) m = fmaxf(m, ld_cluster_f2(mapa(ml + r * 8, p)).x);
+      float l = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (m > -INFINITY)
+        for (int p = 0; p < L.split; ++p) {
+          const float2 x = ld_cluster_f2(mapa(ml + r * 8, p));
+          if (x.y > 0.f) {
+            const float f = ex2_fast(x.x - m);
+            const float4 v = ld_cluster_f4(mapa(base + r * (DH * 4) + ((q ^ (rr & 7)) << 4), p));
+            l += f * x.y;
+            o.x += f * v.x;
+            o.y += f * v.y;
+            o.z += f * v.z;
+            o.w += f * v.w;
+          }
+        }
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      *reinterpret_cast<uint2*>(a.out + (int64_t)(w.q_row0 + t) * a.out_stride + (int64_t)(w.kvh * L.G + g) * DH +
+                                4 * q) = make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
+    }
+    __syncthreads();
+    cluster_arrive();  // no CTA leaves while a peer reads its partials
+    cluster_wait();
+  }
+}
+
+template <int DH>
+cudaError_t launch(const PromptAttnArgs& a, int sm_count, cudaStream_t st) {
+  using C = Cfg<DH>;
+  Launch L;
+  L.G = a.Hq / a.Hkv;
+  L.hc = (L.G + 127) / 128;
+  L.Gc = (L.G + L.hc - 1) / L.hc;
+  L.T = 128 / L.Gc;
+  // sequences with queries, longest key ranges first
+  int n = 0;
+  for (int b = 0; b < a.batch; ++b)
+    if (a.cu_q[b + 1] > a.cu_q[b]) {
+      int i = n++;
+      for (; i > 0 && a.kv_len[L.order[i - 1]] < a.kv_len[b]; --i) L.order[i] = L.order[i - 1];
+      L.order[i] = (uint8_t)b;
+    }
+  L.n_order = n;
+  int64_t units = 0;
+  for (int i = 0; i < n; ++i) {
+    const int b = L.order[i], tok = a.cu_q[b + 1] - a.cu_q[b];
+    L.work_cu[i] = (int)units;
+    units += (int64_t)((tok + L.T * C::NQ - 1) / (L.T * C::NQ)) * a.Hkv * L.hc;
+    if (units > 0x7fffffff / 8) return cudaErrorInvalidConfiguration;
+  }
+  L.work_cu[n] = (int)units;
+  // few units over long key ranges: split the keys over a cluster while every
+  // cluster stays resident and a split keeps four tiles of the longest range
+  const int tiles = (a.kv_len[L.order[0]] + C::BK - 1) / C::BK;
+  L.split = 1;
+  while (L.split < 8 && units * L.split * 2 <= sm_count && tiles >= L.split * 8) L.split *= 2;
+
+  CUtensorMap qmap, kmap, vmap;
+  cudaError_t e = make_bf16_3d_map(&qmap, a.q, {DH, a.Hq, a.cu_q[a.batch]}, {DH, (long)a.q_stride}, {64, L.Gc, L.T});
+  if (e == cudaSuccess)
+    e = make_bf16_3d_map(&kmap, a.k, {64, (long)a.cache_rows, (long)a.Hkv * C::DB}, {(long)a.kv_stride, 64},
+                         {64, C::BK, C::DB});
+  if (e == cudaSuccess)
+    e = make_bf16_3d_map(&vmap, a.v, {64, (long)a.cache_rows, (long)a.Hkv * C::DB}, {(long)a.kv_stride, 64},
+                         {64, C::BK, C::DB});
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * L.split));
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = C::BYTES;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)L.split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = L.split > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, k_prompt_attn<DH>, qmap, kmap, vmap, a, L);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int dh, int sm_count, cudaStream_t s) {
+  if (dh == 64) return launch<64>(a, sm_count, s);
+  if (dh == 128) return launch<128>(a, sm_count, s);
+  return launch<256>(a, sm_count, s);
+}
+
+cudaError_t prompt_kernel_setup() {
+  cudaError_t e = cudaFuncSetAttribute(k_prompt_attn<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<64>::BYTES);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_prompt_attn<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<128>::BYTES);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(k_prompt_attn<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<256>::BYTES);
+  return e;
+}
+
+}  // namespace ae
