@@ -395,8 +395,7 @@ struct TokenAttnArgs {
   int* status;
 };
 cudaError_t launch_token_attention(const TokenAttnArgs& a, int dh, int sm_count, cudaStream_t s);
-// Kernel attributes (shared memory), once per context.
-cudaError_t lm_kernel_setup();
+cudaError_t token_kernel_setup();
 
 // ---- context projection (ae_bind_context)
 // ctx_rope[valid row of request b at position i] = (cos, sin)(i theta^(-2j/dh)).
