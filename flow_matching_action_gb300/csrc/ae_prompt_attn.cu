@@ -44,16 +44,19 @@ struct Cfg {
   static constexpr int SLOT = BK * DH * 2;         // bytes of a K or V tile
   static constexpr int NS = DH == 64 ? 8 : 5;      // ring slots
   static constexpr int QBYTES = 128 * DH * 2;      // bytes of a query tile
-  static constexpr int THREADS = NQ * 128 + 64;
+  static constexpr int THREADS = NQ * 128 + 128;   // + a warpgroup of which two warps work
+  // registers: the softmax warpgroups take what the last one gives back
+  static constexpr int REGS_AUX = 104, REGS_MAX = 200;  // 104 + 2 * 200 = 3 * 168, the launch's registers
   static constexpr int W_LOAD = NQ * 4, W_MMA = NQ * 4 + 1;
   // shared memory, from a 1024-byte boundary
   static constexpr int RING = NQ * QBYTES;
   static constexpr int BARS = RING + NS * SLOT;
   static constexpr int ML = NQ * 128 * DH * 4;     // a split's partial: fp32 rows, then [NQ][128] (m, l)
+  static constexpr int WT = ML + NQ * 128 * 8;     // [rows of this CTA][split] weights of the merge
   static constexpr int BYTES = BARS + 256 + 1024;
   // tensor memory columns
   static constexpr int O0 = 256;
-  static_assert(ML + NQ * 128 * 8 <= BARS, "fp32 partials fit over the tiles");
+  static_assert(WT + NQ * 128 * 4 <= BARS, "fp32 partials fit over the tiles");
   static_assert(BYTES <= 227 * 1024, "shared memory");
 };
 
@@ -117,7 +120,13 @@ __device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.
 __device__ __forceinline__ void landed(uint32_t (&r)[32]) {
   asm volatile("" : AE_U8(r, 0), AE_U8(r, 8), AE_U8(r, 16), AE_U8(r, 24));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      AE_I8(r, 0), AE_I8(r, 8)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
       "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(
@@ -131,14 +140,21 @@ __device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
+               : "r"(addr));
   return v;
 }
 __device__ __forceinline__ float2 ld_cluster_f2(uint32_t addr) {
   float2 v;
   asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
   return v;
+}
+
+// One lane of a converged warp, chosen so that the compiler knows the branch to
+// be uniform: MMA operands then stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // mbar_wait of a whole warp: one answer for all lanes.
@@ -211,7 +227,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars* B = reinterpret_cast<Bars*>(smem + C::BARS);
   volatile int* abort_flag = &B->abort;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = L.split > 1 ? (int)cluster_rank() : 0;
   const Unit w = find_unit<DH>(a, L, blockIdx.x / L.split);
   const uint8_t* mask = a.key_mask ? a.key_mask + w.kv_row0 : nullptr;
@@ -234,7 +250,21 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     n_tiles = max(n_tiles, cnt[s]);
   }
 
-  if (threadIdx.x == 0) {
+  // The load warp sets the barriers up and starts the first copies at once;
+  // the other warps meet it behind them.  The ring holds the tiles in the order
+  // the MMAs use them: K0 V0 K1 V1 .. (NQ = 2), K0 K1 V0 K2 V1 .. (NQ = 1).
+  int loaded = 0;
+  auto load = [&]() {
+    const int i = loaded;
+    const bool is_v = NQ == 2 ? (i & 1) : (i > 0 && ((i & 1) == 0 || i + 1 == 2 * n_tiles));
+    const int t = NQ == 2 ? i >> 1 : (is_v ? (i + 1 == 2 * n_tiles ? n_tiles - 1 : (i >> 1) - 1) : (i + 1) >> 1);
+    const int slot = i % NS;
+    mbar_arrive_expect_tx(&B->full[slot], C::SLOT);
+    tma_load_3d_nohint(smem + C::RING + slot * C::SLOT, is_v ? &vmap : &kmap, &B->full[slot], 0,
+                       (int)(w.kv_row0 + (int64_t)(lo + t) * BK), w.kvh * DB);
+    ++loaded;
+  };
+  if (warp == C::W_LOAD && lane == 0) {
     mbar_init(&B->q, 1);
     mbar_init(&B->drain, 1);
     for (int i = 0; i < 8; ++i) {
@@ -248,6 +278,17 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     }
     *abort_flag = 0;
     fence_mbar_init();
+    fence_proxy_async_smem();
+    if (n_tiles > 0) {
+      mbar_arrive_expect_tx(&B->q, (uint32_t)(NQ * DB * L.T * L.Gc * 128));
+#pragma unroll
+      for (int s = 0; s < NQ; ++s)
+#pragma unroll
+        for (int d = 0; d < DB; ++d)
+          tma_load_3d_nohint(smem + s * C::QBYTES + d * (128 * 128), &qmap, &B->q, d * 64, w.kvh * L.G + w.g0,
+                             w.q_row0 + w.tok0 + s * L.T);
+      while (loaded < NS && loaded < 2 * n_tiles) load();
+    }
   }
   if (warp == C::W_MMA) {
     tmem_alloc(&B->tmem, 512);
@@ -258,36 +299,18 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = B->tmem;
 
+  if (warp >= C::W_LOAD) {
+    if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_AUX));
   if (warp == C::W_LOAD) {
     // ---------------------------------------------------------------- loads
     if (lane == 0 && n_tiles > 0) {
-      mbar_arrive_expect_tx(&B->q, (uint32_t)(NQ * DB * L.T * L.Gc * 128));
-#pragma unroll
-      for (int s = 0; s < NQ; ++s)
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-          tma_load_3d_nohint(smem + s * C::QBYTES + d * (128 * 128), &qmap, &B->q, d * 64,
-                             w.kvh * L.G + w.g0, w.q_row0 + w.tok0 + s * L.T);
-      int c = 0;
-      bool ok = true;
-      auto load = [&](const CUtensorMap* map, int t) {
-        const int slot = c % NS;
-        if (c >= NS) ok = mbar_wait(&B->empty[slot], (uint32_t)((c / NS) & 1) ^ 1u, abort_flag, a.status);
-        if (!ok) return;
-        mbar_arrive_expect_tx(&B->full[slot], C::SLOT);
-        tma_load_3d_nohint(smem + C::RING + slot * C::SLOT, map, &B->full[slot], 0,
-                           (int)(w.kv_row0 + (int64_t)t * BK), w.kvh * DB);
-        ++c;
-      };
-      if (NQ == 1) load(&kmap, lo);
-      for (int i = 0; i < n_tiles && ok; ++i) {
-        if (NQ == 2) load(&kmap, lo + i);
-        else if (i + 1 < n_tiles) load(&kmap, lo + i + 1);
-        if (ok) load(&vmap, lo + i);
-      }
+      while (loaded < 2 * n_tiles &&
+             mbar_wait(&B->empty[loaded % NS], (uint32_t)((loaded / NS) & 1) ^ 1u, abort_flag, a.status))
+        load();
       // every copy lands before the CTA's shared memory is released, also after a failure
       mbar_drain(&B->q, 0, a.status);
-      for (int i = max(0, c - NS); i < c; ++i) mbar_drain(&B->full[i % NS], (uint32_t)(i / NS) & 1u, a.status);
+      for (int i = max(0, loaded - NS); i < loaded; ++i)
+        mbar_drain(&B->full[i % NS], (uint32_t)(i / NS) & 1u, a.status);
     }
   } else if (warp == C::W_MMA) {
     // ---------------------------------------------------------------- MMAs
@@ -295,31 +318,36 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     int c = 0;  // ring slots consumed
     bool ok = n_tiles == 0 || warp_wait(&B->q, 0, abort_flag, a.status);
     auto wait_slot = [&](int i) { return warp_wait(&B->full[i % NS], (uint32_t)(i / NS) & 1u, abort_flag, a.status); };
+    const uint64_t q_desc = sdesc_sw128(smem_u32(smem)), k_desc = sdesc_sw128(smem_u32(smem) + C::RING),
+                   v_desc = sdesc_sw128_mn(smem_u32(smem) + C::RING, BK * 128, 1024);
     auto qk = [&](int s, int buf, int slot) {
-      if (lane == 0) {
+      const uint64_t ad = q_desc + (uint64_t)(s * C::QBYTES >> 4), bd = k_desc + (uint64_t)(slot * C::SLOT >> 4);
+      if (elect_one()) {
 #pragma unroll
-        for (int d = 0; d < DB; ++d) {
-          const uint64_t ad = sdesc_sw128(smem_u32(smem + s * C::QBYTES + d * (128 * 128)));
-          const uint64_t bd = sdesc_sw128(smem_u32(smem + C::RING + slot * C::SLOT + d * (BK * 128)));
+        for (int d = 0; d < DB; ++d)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_bf16(tmem + (uint32_t)(buf * BK), ad + 2 * k, bd + 2 * k, idesc_s, (d > 0 || k > 0) ? 1u : 0u);
-        }
+            mma_bf16(tmem + (uint32_t)(buf * BK), ad + d * (128 * 128 >> 4) + 2 * k, bd + d * (BK * 128 >> 4) + 2 * k,
+                     idesc_s, (d > 0 || k > 0) ? 1u : 0u);
         mma_commit(&B->s[buf]);
       }
+      __syncwarp();
     };
-    auto pv = [&](int s, int buf, int slot, bool first) {
-      if (lane == 0) {
+    auto pv = [&](int s, int buf, int slot, bool first, uint64_t* done) {
+      const uint64_t bd = v_desc + (uint64_t)(slot * C::SLOT >> 4);
+      const uint32_t acc = first ? 0u : 1u;
+      if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < BK / 16; ++k) {
-          const uint64_t bd = sdesc_sw128_mn(smem_u32(smem + C::RING + slot * C::SLOT + k * 2048), BK * 128, 1024);
-          mma_bf16_ts(tmem + (uint32_t)(C::O0 + s * DH), tmem + (uint32_t)(buf * BK + 8 * k), bd, idesc_o,
-                      (!first || k > 0) ? 1u : 0u);
-        }
+        for (int k = 0; k < BK / 16; ++k)
+          mma_bf16_ts(tmem + (uint32_t)(C::O0 + s * DH), tmem + (uint32_t)(buf * BK + 8 * k), bd + k * (2048 >> 4),
+                      idesc_o, k > 0 ? 1u : acc);
+        if (done != nullptr) mma_commit(done);
       }
+      __syncwarp();
     };
     auto release = [&](int slot) {
-      if (lane == 0) mma_commit(&B->empty[slot]);
+      if (elect_one()) mma_commit(&B->empty[slot]);
+      __syncwarp();
     };
     // zero the V rows of tile i that no query may see
     auto clean_v = [&](int i, int slot) {
@@ -359,19 +387,14 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
         // slot c: V of tile i, slot c + 1: K of tile i + 1
         if (!(ok = wait_slot(c))) break;
         clean_v(i, c % NS);
-        bool have_k = false;
+        if (i + 1 < n_tiles && !(ok = wait_slot(c + 1))) break;
 #pragma unroll
         for (int s = 0; s < NQ; ++s) {
           if (ok && i < cnt[s]) {
             if (!(ok = warp_wait(&B->p[s], (uint32_t)i & 1u, abort_flag, a.status))) break;
             tc_fence_after();
-            pv(s, s, c % NS, i == 0);
-            if (i + 1 == cnt[s] && lane == 0) mma_commit(&B->o[s]);
-          }
-          if (ok && i + 1 < cnt[s]) {
-            if (!have_k && !(ok = wait_slot(c + 1))) break;
-            have_k = true;
-            qk(s, s, (c + 1) % NS);
+            pv(s, s, c % NS, i == 0, i + 1 == cnt[s] ? &B->o[s] : nullptr);
+            if (i + 1 < cnt[s]) qk(s, s, (c + 1) % NS);
           }
         }
         if (!ok) break;
@@ -396,8 +419,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
         clean_v(i, c % NS);
         if (!(ok = warp_wait(&B->p[i & 1], (uint32_t)(i >> 1) & 1u, abort_flag, a.status))) break;
         tc_fence_after();
-        pv(0, i & 1, c % NS, i == 0);
-        if (lane == 0) mma_commit(&B->o[i & 1]);
+        pv(0, i & 1, c % NS, i == 0, &B->o[i & 1]);
         release(c % NS);
         ++c;
       }
@@ -407,8 +429,10 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
       mbar_drain(&B->drain, 0, a.status);
     }
     __syncwarp();
+  }
   } else {
     // ---------------------------------------------------------------- softmax
+    if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_MAX));
     const int s = warp >> 2;             // query tile of this warpgroup
     const int row = threadIdx.x & 127;   // its row, the TMEM lane
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
@@ -423,7 +447,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     const uint32_t tm_o = tmem + lane_off + (uint32_t)(C::O0 + s * DH);
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    const int n = cnt[NQ == 1 ? 0 : s];
+    const int n = s == 0 ? cnt[0] : cnt[NQ - 1];
     for (int i = 0; i < n; ++i) {
       const int buf = NQ == 1 ? i & 1 : s;
       const uint32_t tm_s = tmem + lane_off + (uint32_t)(buf * BK);
@@ -441,24 +465,25 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
       }
       tc_fence_after();
       uint32_t sc[BK / 32][32];
+      float mx[8];
 #pragma unroll
-      for (int k = 0; k < BK / 32; ++k) tmem_ld32_start(tm_s + 32 * k, sc[k]);
-      tmem_ld_wait();
+      for (int e = 0; e < 8; ++e) mx[e] = -INFINITY;
+      tmem_ld32_start(tm_s, sc[0]);
 #pragma unroll
-      for (int k = 0; k < BK / 32; ++k) landed(sc[k]);
-      if (partial) {
-#pragma unroll
-        for (int k = 0; k < BK / 32; ++k)
+      for (int k = 0; k < BK / 32; ++k) {  // the next 32 scores arrive under this maximum
+        tmem_ld_wait();
+        landed(sc[k]);
+        if (k + 1 < BK / 32) tmem_ld32_start(tm_s + 32 * (k + 1), sc[k + 1]);
+        if (partial) {
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if (!((bits[k] >> j) & 1u)) sc[k][j] = 0xff800000u;  // -inf
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) mx[j & 7] = fmaxf(mx[j & 7], __uint_as_float(sc[k][j]));
       }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int k = 0; k < BK / 32; ++k)
-#pragma unroll
-        for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(sc[k][j]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * c;
+      const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
+                              fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * c;
       float factor = 1.f;
       if (top > m + kRaise) {  // -inf stays -inf while no key has been seen
         factor = ex2_fast(m - top);
@@ -481,7 +506,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
           landed(o);
 #pragma unroll
           for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * factor);
-          tmem_st32(tm_o + d, o);
+          tmem_st(tm_o + d, o);
         }
         tmem_st_wait();
       }
@@ -489,11 +514,12 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
       const uint64_t c2 = pack2(c, c), b2 = pack2(base, base);
       uint64_t sum[2] = {0, 0};
 #pragma unroll
-      for (int h = 0; h < BK / 64; ++h) {
-        uint32_t p[32];
+      for (int h = 0; h < 2; ++h) {
+        constexpr int HK = BK / 2;
+        uint32_t p[HK / 2];
 #pragma unroll
-        for (int j = 0; j < 64; j += 2) {
-          const int k = 2 * h + (j >> 5), e = j & 31;
+        for (int j = 0; j < HK; j += 2) {
+          const int k = (h * HK + j) >> 5, e = (h * HK + j) & 31;
           float x, y;
           unpack2(fma2(pack2(__uint_as_float(sc[k][e]), __uint_as_float(sc[k][e + 1])), c2, b2), x, y);
           x = ex2_fast(x);
@@ -501,7 +527,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
           sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pack2(x, y));
           p[j >> 1] = bf16x2(x, y);
         }
-        tmem_st32(tm_s + 32 * h, p);  // over S columns read above
+        tmem_st(tm_s + (HK / 2) * h, p);  // over S columns read above
       }
       float x, y;
       unpack2(add2(sum[0], sum[1]), x, y);
@@ -572,36 +598,58 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     __syncwarp();
     cluster_arrive();
     cluster_wait();
-    // rank r merges its share of the rows, DH / 4 lanes-of-four per row
-    const int rows = NQ * 128, share = rows / L.split;
-    constexpr int PER = DH / 4;
+    // rank r merges its share of the rows: the weight 2^(m_p - m) / l of every
+    // split first, then DH / 4 four-dim pieces a row, four pieces a thread at once
+    const int share = NQ * 128 / L.split;
+    constexpr int PER = DH / 4, UN = 4;
     const uint32_t base = smem_u32(smem), ml = smem_u32(smem + C::ML);
-    for (int i = threadIdx.x; i < share * PER; i += C::THREADS) {
-      const int r = rank * share + i / PER, q = i % PER;
-      const int s = r >> 7, rr = r & 127;
-      const int tok = rr / L.Gc, g = w.g0 + rr - tok * L.Gc;
-      const int t = w.tok0 + s * L.T + tok;
-      if (tok >= L.T || t >= w.n_new || g >= L.G) continue;
-      float m = -INFINITY;
-      for (int p = 0; p < L.split; ++p) m = fmaxf(m, ld_cluster_f2(mapa(ml + r * 8, p)).x);
-      float l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (m > -INFINITY)
-        for (int p = 0; p < L.split; ++p) {
-          const float2 x = ld_cluster_f2(mapa(ml + r * 8, p));
-          if (x.y > 0.f) {
-            const float f = ex2_fast(x.x - m);
-            const float4 v = ld_cluster_f4(mapa(base + r * (DH * 4) + ((q ^ (rr & 7)) << 4), p));
-            l += f * x.y;
-            o.x += f * v.x;
-            o.y += f * v.y;
-            o.z += f * v.z;
-            o.w += f * v.w;
-          }
+    float* wt = reinterpret_cast<float*>(smem + C::WT);  // [share][split]
+    for (int i = threadIdx.x; i < share; i += C::THREADS) {
+      const int r = rank * share + i;
+      float2 x[8];
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        x[p] = p < L.split ? ld_cluster_f2(mapa(ml + r * 8, p)) : make_float2(-INFINITY, 0.f);
+        m = fmaxf(m, x[p].x);
+      }
+#pragma unroll
+      for (int p = 0; p < 8; ++p) {
+        x[p].x = x[p].y > 0.f ? ex2_fast(x[p].x - m) : 0.f;
+        l += x[p].x * x[p].y;
+      }
+#pragma unroll
+      for (int p = 0; p < 8; ++p)
+        if (p < L.split) wt[i * L.split + p] = l > 0.f ? x[p].x / l : 0.f;
+    }
+    __syncthreads();
+    for (int i0 = threadIdx.x; i0 < share * PER; i0 += UN * C::THREADS) {
+      float4 o[UN];
+#pragma unroll
+      for (int e = 0; e < UN; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int p = 0; p < L.split; ++p) {
+        const uint32_t peer = mapa(base, p);
+#pragma unroll
+        for (int e = 0; e < UN; ++e) {
+          const int i = min(i0 + e * C::THREADS, share * PER - 1), r = rank * share + i / PER, q = i % PER;
+          const float4 v = ld_cluster_f4(peer + r * (DH * 4) + ((q ^ (r & 7)) << 4));
+          const float f = wt[(i / PER) * L.split + p];
+          o[e].x += f * v.x;
+          o[e].y += f * v.y;
+          o[e].z += f * v.z;
+          o[e].w += f * v.w;
         }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      *reinterpret_cast<uint2*>(a.out + (int64_t)(w.q_row0 + t) * a.out_stride + (int64_t)(w.kvh * L.G + g) * DH +
-                                4 * q) = make_uint2(bf16x2(o.x * inv, o.y * inv), bf16x2(o.z * inv, o.w * inv));
+      }
+#pragma unroll
+      for (int e = 0; e < UN; ++e) {
+        const int i = i0 + e * C::THREADS, r = rank * share + i / PER, q = i % PER;
+        const int s = r >> 7, rr = r & 127;
+        const int tok = rr / L.Gc, g = w.g0 + rr - tok * L.Gc;
+        const int t = w.tok0 + s * L.T + tok;
+        if (i >= share * PER || tok >= L.T || t >= w.n_new || g >= L.G) continue;
+        *reinterpret_cast<uint2*>(a.out + (int64_t)(w.q_row0 + t) * a.out_stride + (int64_t)(w.kvh * L.G + g) * DH +
+                                  4 * q) = make_uint2(bf16x2(o[e].x, o[e].y), bf16x2(o[e].z, o[e].w));
+      }
     }
     __syncthreads();
     cluster_arrive();  // no CTA leaves while a peer reads its partials
