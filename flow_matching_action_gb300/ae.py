@@ -83,6 +83,14 @@ class ae_token_attention_args(ctypes.Structure):
                 ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64)]
 
 
+class ae_prefill_prompts_args(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("causal", ctypes.c_int), ("cu_lens", ctypes.c_void_p),
+                ("embeddings", ctypes.c_void_p), ("token_mask", ctypes.c_void_p), ("n_axes", ctypes.c_int),
+                ("positions", ctypes.c_void_p), ("pair_axis", ctypes.c_char_p), ("pair_freq", ctypes.c_void_p),
+                ("q_norm", ctypes.c_void_p), ("k_norm", ctypes.c_void_p), ("norm_offset", ctypes.c_float),
+                ("out_k", ctypes.c_void_p), ("out_v", ctypes.c_void_p)]
+
+
 # Every symbol include/ae.h declares, with its ctypes signature.
 _SIGNATURES = {
     "ae_create": (ctypes.c_int, [ctypes.POINTER(ae_config), ctypes.POINTER(ae_weights), ctypes.c_int,
@@ -99,6 +107,7 @@ _SIGNATURES = {
     "ae_qk_norm_rope": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ae_qk_norm_rope_args)]),
     "ae_prompt_attention": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ae_prompt_attention_args)]),
     "ae_token_attention": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ae_token_attention_args)]),
+    "ae_prefill_prompts": (ctypes.c_int, [ctypes.c_void_p, ctypes.POINTER(ae_prefill_prompts_args)]),
     "ae_sample": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]),
     "ae_sample_noalloc": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]),
     "ae_set_debug_dump": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t]),
@@ -229,6 +238,10 @@ def ae_token_attention(ctx, args: ae_token_attention_args) -> None:
     _check(lib().ae_token_attention(ctx, ctypes.byref(args)), ctx)
 
 
+def ae_prefill_prompts(ctx, args: ae_prefill_prompts_args) -> None:
+    _check(lib().ae_prefill_prompts(ctx, ctypes.byref(args)), ctx)
+
+
 def _rows(name: str, t, width: int, rows: Optional[int] = None):
     """(pointer, row stride) of a bf16 CUDA tensor [rows, width] whose rows are contiguous."""
     if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows):
@@ -259,6 +272,18 @@ def _host_array(ctype, x):
 
 def _addr(arr):
     return None if arr is None else ctypes.addressof(arr)
+
+
+def _pairs(pair_axis, pair_freq, half: int):
+    """(bytes of the axes, array of the frequencies) of dh / 2 rotation pairs, None as given."""
+    if pair_axis is not None:
+        if len(pair_axis) != half:
+            raise ValueError(f"pair_axis: {len(pair_axis)} entries, expected {half}")
+        pair_axis = pair_axis if isinstance(pair_axis, bytes) else bytes(pair_axis)
+    freq = _host_array(ctypes.c_double, pair_freq)
+    if freq is not None and len(freq) != half:
+        raise ValueError(f"pair_freq: {len(freq)} entries, expected {half}")
+    return pair_axis, freq
 
 
 def ae_sample(ctx, noise, n_steps: int, out_actions) -> None:
@@ -354,15 +379,7 @@ class ActionExpert:
         a.k_norm = _vec("k_norm", k_norm, "torch.bfloat16", d.head_dim)
         a.norm_offset = norm_offset
         a.positions = _vec("positions", positions, "torch.int32", a.n_axes * n)
-        half = d.head_dim // 2
-        if pair_axis is not None:
-            if len(pair_axis) != half:
-                raise ValueError(f"pair_axis: {len(pair_axis)} entries, expected {half}")
-            # a bytes object of at least `half` entries; ctypes passes its buffer
-            a.pair_axis = pair_axis if isinstance(pair_axis, bytes) else bytes(pair_axis)
-        freq = _host_array(ctypes.c_double, pair_freq)
-        if freq is not None and len(freq) != half:
-            raise ValueError(f"pair_freq: {len(freq)} entries, expected {half}")
+        a.pair_axis, freq = _pairs(pair_axis, pair_freq, d.head_dim // 2)
         a.pair_freq = _addr(freq)
         a.kv_rows = _vec("kv_rows", kv_rows, "torch.int64", n)
         a.q_out, a.q_stride = _rows("q_out", q_out, d.q_dim, n)
@@ -431,6 +448,38 @@ class ActionExpert:
         a.out, a.out_stride = _rows("out", out, d.q_dim, n)
         ae_token_attention(self.ctx, a)
         return out
+
+    def prefill_prompts(self, embeddings, cu_lens, positions, out_k, out_v, causal: bool = True, token_mask=None,
+                        q_norm=None, k_norm=None, norm_offset: float = 0.0, pair_axis=None, pair_freq=None):
+        """VLM prefill of packed prompts (see include/ae.h): K and V of every layer into out_k / out_v.
+
+        embeddings [total, width] bf16; positions int32 [total] or [axes, total]; out_k / out_v
+        [layers, total, Hkv dh] bf16; q_norm / k_norm one bf16 [dh] tensor a layer.
+        """
+        d = self.dims
+        cu = _host_array(ctypes.c_int32, cu_lens)
+        n = embeddings.shape[0]
+        if cu[len(cu) - 1] != n:
+            raise ValueError(f"embeddings: {n} rows, cu_lens ends at {cu[len(cu) - 1]}")
+        a = ae_prefill_prompts_args()
+        a.batch, a.causal, a.cu_lens = len(cu) - 1, 1 if causal else 0, _addr(cu)
+        a.embeddings = _vec("embeddings", embeddings, "torch.bfloat16", n * d.width)
+        a.token_mask = _vec("token_mask", token_mask, "torch.uint8", n)
+        a.n_axes = positions.shape[0] if positions.dim() == 2 else 1
+        a.positions = _vec("positions", positions, "torch.int32", a.n_axes * n)
+        a.pair_axis, freq = _pairs(pair_axis, pair_freq, d.head_dim // 2)
+        a.pair_freq = _addr(freq)
+        norms = []
+        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if w is not None and len(w) != d.layers:
+                raise ValueError(f"{name}: {len(w)} tensors for {d.layers} layers")
+            norms.append(None if w is None else (ctypes.c_void_p * d.layers)(
+                *[_vec(name, x, "torch.bfloat16", d.head_dim) for x in w]))
+        a.q_norm, a.k_norm = _addr(norms[0]), _addr(norms[1])
+        a.norm_offset = norm_offset
+        a.out_k = _vec("out_k", out_k, "torch.bfloat16", d.layers * n * d.kv_dim)
+        a.out_v = _vec("out_v", out_v, "torch.bfloat16", d.layers * n * d.kv_dim)
+        ae_prefill_prompts(self.ctx, a)
 
     def sample(self, noise, n_steps: int, out=None):
         if out is None:

@@ -400,6 +400,7 @@ ae_status sticky(const ae_ctx* c) {
 }  // namespace
 
 namespace ae {
+ae_status ensure_time_table(ae_ctx* c, int n_steps, const TimeTable** out) { return get_table(c, n_steps, out); }
 const TimeTable* find_time_table(const ae_ctx* c, int n_steps) {
   for (const TimeTable& t : c->tables)
     if (t.n_steps == n_steps) return &t;

@@ -190,7 +190,8 @@ int launch_step_fast(ae_ctx* c, const TimeTable& t, int step, float* x, cudaStre
                      cudaError_t* err, const AttnScratch* attn_scratch, const PrefillOut* prefill) {
   const bool pdl = c->pdl;
   const Dims& d = c->d;
-  const int B = c->bind.batch, M = B * d.H, D = d.D, F = d.F, L = d.L;
+  const bool prompts = prefill != nullptr && prefill->rope != nullptr;
+  const int B = c->bind.batch, M = prompts ? prefill->rope->tokens : B * d.H, D = d.D, F = d.F, L = d.L;
   const int nqkv = d.qkvdim(), qd = d.qdim();
   const float eps = (float)d.eps;
   const int sm = c->sm_count;
@@ -236,7 +237,7 @@ int launch_step_fast(ae_ctx* c, const TimeTable& t, int step, float* x, cudaStre
     a.eps = eps;
     a.rope_cs = c->rope_cs;
     a.dh = d.dh;
-    a.n_rot_heads = d.Hq + d.Hkv;
+    a.n_rot_heads = prompts ? 0 : d.Hq + d.Hkv;
     a.act_rows = box_m;
     return a;
   };
@@ -267,7 +268,17 @@ int launch_step_fast(ae_ctx* c, const TimeTable& t, int step, float* x, cudaStre
     a.out_bf16 = qkv;
     ck(launch_tc_gemm(c->map_qkv, c->map_yq, pq, a, s, pdl));
     ++n;
-    if (prefill != nullptr) {
+    if (prompts) {
+      // norms and rotation in place on the queries, K and V into the prefix layout
+      RopeNormArgs& r = *prefill->rope;
+      r.q_norm = prefill->q_norm ? (const bf16*)prefill->q_norm[l] : nullptr;
+      r.k_norm = prefill->k_norm ? (const bf16*)prefill->k_norm[l] : nullptr;
+      r.k_cache = prefill->k + (size_t)l * M * d.kvdim();
+      r.v_cache = prefill->v + (size_t)l * M * d.kvdim();
+      ck(launch_qk_norm_rope(r, d.dh, sm, s));
+      ++n;
+      if (l + 1 == L) break;  // nothing after the last layer's K/V is an output
+    } else if (prefill != nullptr) {
       // this layer's K (rotated) and V: columns [Hq dh, (Hq + Hkv) dh) and the
       // next Hkv dh of the q|k|v rows, into the prefix layout [L][M][Hkv dh]
       const size_t kvd = d.kvdim(), row = (size_t)nqkv * sizeof(bf16);
@@ -279,8 +290,14 @@ int launch_step_fast(ae_ctx* c, const TimeTable& t, int step, float* x, cudaStre
       if (l + 1 == L) break;  // nothing after the last layer's K/V is an output
     }
 
-    // attention over [valid prefix || actions]
-    {
+    if (prompts) {
+      PromptAttnArgs& p = *prefill->attn;
+      p.k = prefill->rope->k_cache;
+      p.v = prefill->rope->v_cache;
+      ck(launch_prompt_attention(p, d.dh, sm, s));
+      ++n;
+    } else {
+      // attention over [valid prefix || actions]
       AttnArgs at = {};
       const long lay = (long)l * c->bind.total_rows * d.kvdim();
       at.qkv = qkv;

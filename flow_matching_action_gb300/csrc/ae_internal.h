@@ -423,14 +423,24 @@ struct AttnScratch {
 // A prefill run of the layers (ae_prefill): embeddings replace the action
 // input projection, every layer's K and V are copied out after its QKV GEMM,
 // and nothing after the last layer's QKV GEMM runs.
+// With `rope` (ae_prefill_prompts) the tokens are packed prompts: queries and
+// keys are normed and rotated by the operator, which also writes K and V out,
+// and the attention is the prompts' own.  The templates hold what does not
+// change between layers.
 struct PrefillOut {
   const bf16* emb;  // [M][D]
   bf16* k;          // [L][M][Hkv dh]
   bf16* v;
+  RopeNormArgs* rope = nullptr;
+  PromptAttnArgs* attn = nullptr;
+  const void* const* q_norm = nullptr;  // host [L] or nullptr
+  const void* const* k_norm = nullptr;
 };
 int launch_step_fast(ae_ctx* c, const TimeTable& t, int step, float* x, cudaStream_t s,
                      cudaError_t* err, const AttnScratch* attn_scratch = nullptr,
                      const PrefillOut* prefill = nullptr);
+// The time table of n_steps, built on first use (allocates).
+ae_status ensure_time_table(ae_ctx* c, int n_steps, const TimeTable** out);
 // The cached time table of n_steps, or nullptr (never allocates).
 const TimeTable* find_time_table(const ae_ctx* c, int n_steps);
 void attn_plan(AttnArgs& a, int sm_count);

@@ -51,6 +51,27 @@ ae_status check_scale(ae_ctx* c, float scale) {
   return AE_OK;
 }
 
+ae_status check_rotation(ae_ctx* c, int n_axes, const uint8_t* pair_axis, const double* pair_freq) {
+  const int half = c->d.dh / 2;
+  if (n_axes < 1 || n_axes > AE_MAX_AXES)
+    return fail(c, AE_ERR_SHAPE, "n_axes %d outside 1..%d", n_axes, AE_MAX_AXES);
+  if (pair_axis != nullptr)
+    for (int j = 0; j < half; ++j)
+      if (pair_axis[j] >= n_axes)
+        return fail(c, AE_ERR_INVALID_ARG, "pair_axis[%d] = %d, n_axes is %d", j, pair_axis[j], n_axes);
+  if (pair_freq != nullptr)
+    for (int j = 0; j < half; ++j)
+      if (!isfinite(pair_freq[j])) return fail(c, AE_ERR_INVALID_ARG, "pair_freq[%d] is not finite", j);
+  return AE_OK;
+}
+
+void set_rotation(const ae_ctx* c, ae::RopeNormArgs* a, const uint8_t* pair_axis, const double* pair_freq) {
+  for (int j = 0; j < c->d.dh / 2; ++j) {
+    a->axis[j] = pair_axis ? pair_axis[j] : 0;
+    a->turn[j] = pair_freq ? ae::turn_fraction(pair_freq[j]) : c->rope_turn[j];
+  }
+}
+
 // Checks common to the operators.  `op` names the call.
 ae_status check_context(ae_ctx* c, const void* args, const char* op) {
   if (args == nullptr) return fail(c, AE_ERR_INVALID_ARG, "%s: args is NULL", op);
@@ -98,17 +119,9 @@ ae_status ae_qk_norm_rope(ae_ctx* c, const ae_qk_norm_rope_args* p) {
   AE_TRY(check_context(c, p, op));
   const ae::Dims& d = c->d;
   if (p->tokens < 0) return fail(c, AE_ERR_SHAPE, "tokens %d < 0", p->tokens);
-  if (p->n_axes < 1 || p->n_axes > AE_MAX_AXES)
-    return fail(c, AE_ERR_SHAPE, "n_axes %d outside 1..%d", p->n_axes, AE_MAX_AXES);
   if (!isfinite(p->norm_offset)) return fail(c, AE_ERR_INVALID_ARG, "norm_offset must be finite");
   AE_TRY(check_cache_rows(c, p->cache_rows));
-  if (p->pair_axis != nullptr)
-    for (int j = 0; j < d.dh / 2; ++j)
-      if (p->pair_axis[j] >= p->n_axes)
-        return fail(c, AE_ERR_INVALID_ARG, "pair_axis[%d] = %d, n_axes is %d", j, p->pair_axis[j], p->n_axes);
-  if (p->pair_freq != nullptr)
-    for (int j = 0; j < d.dh / 2; ++j)
-      if (!isfinite(p->pair_freq[j])) return fail(c, AE_ERR_INVALID_ARG, "pair_freq[%d] is not finite", j);
+  AE_TRY(check_rotation(c, p->n_axes, p->pair_axis, p->pair_freq));
   if (p->tokens == 0) return AE_OK;
   if (p->kv_rows == nullptr && p->tokens > p->cache_rows)
     return fail(c, AE_ERR_SHAPE, "%d tokens, %lld cache rows", p->tokens, (long long)p->cache_rows);
@@ -144,10 +157,7 @@ ae_status ae_qk_norm_rope(ae_ctx* c, const ae_qk_norm_rope_args* p) {
   a.v_cache = (ae::bf16*)p->v_cache;
   a.kv_stride = p->kv_stride;
   a.status = c->status_dev;
-  for (int j = 0; j < d.dh / 2; ++j) {
-    a.axis[j] = p->pair_axis ? p->pair_axis[j] : 0;
-    a.turn[j] = p->pair_freq ? ae::turn_fraction(p->pair_freq[j]) : c->rope_turn[j];
-  }
+  set_rotation(c, &a, p->pair_axis, p->pair_freq);
   return launched(c, ae::launch_qk_norm_rope(a, d.dh, c->sm_count, c->stream), op);
 }
 
@@ -250,6 +260,81 @@ ae_status ae_token_attention(ae_ctx* c, const ae_token_attention_args* p) {
   a.out = (ae::bf16*)p->out;
   a.status = c->status_dev;
   return launched(c, ae::launch_token_attention(a, d.dh, c->sm_count, c->stream), op);
+}
+
+ae_status ae_prefill_prompts(ae_ctx* c, const ae_prefill_prompts_args* p) {
+  if (c == nullptr) return AE_ERR_INVALID_ARG;
+  const char* op = "ae_prefill_prompts";
+  AE_TRY(check_context(c, p, op));
+  const ae::Dims& d = c->d;
+  if (p->batch < 0 || p->batch > AE_MAX_BATCH)
+    return fail(c, AE_ERR_SHAPE, "batch %d outside 0..%d", p->batch, AE_MAX_BATCH);
+  if (!isfinite(p->norm_offset)) return fail(c, AE_ERR_INVALID_ARG, "norm_offset must be finite");
+  AE_TRY(check_rotation(c, p->n_axes, p->pair_axis, p->pair_freq));
+  if (p->batch == 0) return AE_OK;
+  if (p->cu_lens == nullptr) return fail(c, AE_ERR_INVALID_ARG, "cu_lens is NULL");
+  if (p->cu_lens[0] != 0) return fail(c, AE_ERR_SHAPE, "cu_lens[0] must be 0");
+  ae::PromptAttnArgs at = {};
+  for (int b = 0; b < p->batch; ++b) {
+    if (p->cu_lens[b + 1] < p->cu_lens[b]) return fail(c, AE_ERR_SHAPE, "cu_lens decreases at sequence %d", b);
+    at.cu_q[b] = p->cu_lens[b];
+    at.kv_row0[b] = p->cu_lens[b];
+    at.kv_len[b] = p->cu_lens[b + 1] - p->cu_lens[b];
+  }
+  const int total = p->cu_lens[p->batch];
+  at.cu_q[p->batch] = total;
+  if (total > (int64_t)c->max_batch * d.H)
+    return fail(c, AE_ERR_SHAPE, "%d tokens > max_batch * horizon = %lld", total, (long long)c->max_batch * d.H);
+  if (total == 0) return AE_OK;
+  AE_TRY(check_rows(c, "embeddings", p->embeddings, d.D, d.D));
+  AE_TRY(check_rows(c, "out_k", p->out_k, d.kvdim(), d.kvdim()));
+  AE_TRY(check_rows(c, "out_v", p->out_v, d.kvdim(), d.kvdim()));
+  if (p->positions == nullptr) return fail(c, AE_ERR_INVALID_ARG, "positions is NULL");
+  if ((uintptr_t)p->positions % 4 != 0)
+    return fail(c, AE_ERR_INVALID_ARG, "positions is not aligned to its elements");
+  for (const void* const* w : {p->q_norm, p->k_norm})
+    if (w != nullptr)
+      for (int l = 0; l < d.L; ++l)
+        if (w[l] == nullptr || (uintptr_t)w[l] % 16 != 0)
+          return fail(c, AE_ERR_INVALID_ARG, "norm weight of layer %d is NULL or not 16-byte aligned", l);
+  AE_TRY(check_device(c));
+  const ae::TimeTable* t = nullptr;
+  AE_TRY(ae::ensure_time_table(c, 1, &t));  // constant conditioning: the modulation biases
+
+  ae::RopeNormArgs r = {};
+  r.tokens = total;
+  r.n_axes = p->n_axes;
+  r.Hq = at.Hq = d.Hq;
+  r.Hkv = at.Hkv = d.Hkv;
+  r.qkv = (const ae::bf16*)c->qkv;
+  r.qkv_stride = d.qkvdim();
+  r.norm_offset = p->norm_offset;
+  r.eps = (float)d.eps;
+  r.positions = p->positions;
+  r.cache_rows = total;
+  r.q_out = (ae::bf16*)c->qkv;  // in place
+  r.q_stride = d.qkvdim();
+  r.kv_stride = d.kvdim();
+  r.status = at.status = c->status_dev;
+  set_rotation(c, &r, p->pair_axis, p->pair_freq);
+  at.batch = p->batch;
+  at.causal = p->causal != 0;
+  at.cache_rows = total;
+  at.q = (const ae::bf16*)c->qkv;
+  at.q_stride = d.qkvdim();
+  at.kv_stride = d.kvdim();
+  at.out = (ae::bf16*)c->o;
+  at.out_stride = d.qdim();
+  at.key_mask = p->token_mask;
+  at.scale = (float)(1.0 / sqrt((double)d.dh));
+  ae::PrefillOut po{(const ae::bf16*)p->embeddings, (ae::bf16*)p->out_k, (ae::bf16*)p->out_v};
+  po.rope = &r;
+  po.attn = &at;
+  po.q_norm = p->q_norm;
+  po.k_norm = p->k_norm;
+  cudaError_t e = cudaSuccess;
+  c->launches_sample = ae::launch_step_fast(c, *t, 0, nullptr, c->stream, &e, nullptr, &po);
+  return launched(c, e, op);
 }
 
 }  // extern "C"

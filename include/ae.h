@@ -374,6 +374,40 @@ typedef struct {
 AE_API ae_status ae_token_attention(ae_ctx* ctx, const ae_token_attention_args* args);
 
 /*
+ * VLM prefill of packed prompts of different lengths (the pages' VLM backbone
+ * is a causal decoder whose requests differ in images and instruction; OxyGen:
+ * one prefill serves the action and the language expert).  As ae_prefill (same
+ * layer, same context description), with the attention of the operators above:
+ * every sequence's tokens attend to each other, causally or not, without the
+ * masked ones; queries and keys are normed per head when norm weights are given
+ * and rotated at the given positions; K (rotated) and V of every layer go to
+ * out_k / out_v in the packed layout ae_bind_prefix, ae_prompt_attention and
+ * ae_token_attention read.  The projections are rounded to bf16 before the norm.
+ * The binding of the context is left as it is.  Allocates the conditioning
+ * table on the context's first prefill only.
+ * Errors: AE_ERR_UNSUPPORTED (fp32 context), AE_ERR_SHAPE (batch outside
+ * 0..AE_MAX_BATCH, more than max_batch * horizon tokens, bad cu_lens or axes),
+ * AE_ERR_INVALID_ARG, AE_ERR_DEVICE, AE_ERR_OOM, AE_ERR_CUDA.
+ */
+typedef struct {
+  int batch;
+  int causal;
+  const int32_t* cu_lens;    /* HOST [batch + 1], cu_lens[0] == 0, non-decreasing */
+  const void* embeddings;    /* device bf16 [total][width], total = cu_lens[batch] */
+  const uint8_t* token_mask; /* device [total], 0 = never attended to (its embedding may hold
+                                anything); NULL: none */
+  int n_axes;                /* positions and rotation as in ae_qk_norm_rope      */
+  const int32_t* positions;  /* device [n_axes][total]                           */
+  const uint8_t* pair_axis;
+  const double* pair_freq;
+  const void* const* q_norm; /* HOST [layers] device bf16 [dh] norm weights, or NULL */
+  const void* const* k_norm;
+  float norm_offset;
+  void *out_k, *out_v;       /* device bf16 [layers][total][n_kv_heads * head_dim] */
+} ae_prefill_prompts_args;
+AE_API ae_status ae_prefill_prompts(ae_ctx* ctx, const ae_prefill_prompts_args* args);
+
+/*
  * Run n_steps Euler steps of delta = -1/n_steps from t = 1 for every bound
  * request (MolmoBot Part 2), the velocity of step k taken at t = 1 - k/n_steps.
  *   noise        device fp32 [batch][horizon][action_dim], the state at t = 1

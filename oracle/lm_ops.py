@@ -60,3 +60,32 @@ def packed_attention(q, k, v, hq, hkv, cu_q, row0, lens, mask=None, causal=True,
             g = slice((h // (hq // hkv)) * dh, (h // (hq // hkv) + 1) * dh)
             out[q0:q1, c], mag[q0:q1, c] = attend(q[q0:q1, c], kb[:, g], vb[:, g], seen, scale)
     return out, mag
+
+
+def prefill_prompts(dims, w, emb, cu, positions, axis, freq, causal=True, mask=None, q_norm=None, k_norm=None,
+                    offset=0.0):
+    """Per-layer K and V of a VLM prefill over packed prompts (the layer of
+    ``ae_oracle.prefill_request`` with per-head norms, several rotary axes and
+    a causal or bidirectional attention within each prompt).
+    emb [tokens, D] -> (K, V) [L, tokens, hkv * dh]."""
+    from .ae_oracle import ada_rms, gelu_tanh, modulation
+    n, D = emb.shape
+    L, hq, hkv, dh = dims.layers, dims.n_q_heads, dims.n_kv_heads, dims.head_dim
+    f = lambda x: np.asarray(x, dtype=np.float64)  # noqa: E731
+    ks, vs = np.empty((L, n, hkv * dh)), np.empty((L, n, hkv * dh))
+    lens = [cu[b + 1] - cu[b] for b in range(len(cu) - 1)]
+    h = f(emb)
+    for l in range(L):
+        s1, sh1, g1 = modulation(np.zeros(D), w["w_mod1"][l], w["b_mod1"][l], 3)
+        s2, sh2, g2 = modulation(np.zeros(D), w["w_mod2"][l], w["b_mod2"][l], 3)
+        y = ada_rms(h, s1, sh1, dims.rms_eps)
+        q, k, v = y @ f(w["wq"][l]).T, y @ f(w["wk"][l]).T, y @ f(w["wv"][l]).T
+        rot = lambda x, heads, nw: norm_rope(x.reshape(n, heads, dh), None if nw is None else nw[l], offset,  # noqa
+                                             dims.rms_eps, positions, axis, freq).reshape(n, heads * dh)
+        q, k = rot(q, hq, q_norm), rot(k, hkv, k_norm)
+        ks[l], vs[l] = k, v
+        o, _ = packed_attention(q, k, v, hq, hkv, cu, cu[:-1], lens, mask, causal)
+        h = h + g1 * (o @ f(w["wo"][l]).T)
+        y2 = ada_rms(h, s2, sh2, dims.rms_eps)
+        h = h + g2 * ((gelu_tanh(y2 @ f(w["wg"][l]).T) * (y2 @ f(w["wu"][l]).T)) @ f(w["wd"][l]).T)
+    return ks, vs

@@ -70,6 +70,16 @@ def token_args(**kw):
     return a
 
 
+def prefill_args(cu=(0, 2, 4), **kw):
+    a = ae.ae_prefill_prompts_args(batch=len(cu) - 1, causal=1, embeddings=FAKE, n_axes=1, positions=FAKE, out_k=FAKE,
+                                   out_v=FAKE)
+    a._keep = i32(*cu)
+    a.cu_lens = ae._addr(a._keep)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
 def refused(call, ctx, args, status):
     with pytest.raises(ae.AEError) as e:
         call(ctx, args)
@@ -120,7 +130,23 @@ def test_token_attention_refuses(make_context, kw, status):
     refused(ae.ae_token_attention, make_context(), token_args(**kw), status)
 
 
-@pytest.mark.parametrize("call,args", [(ae.ae_qk_norm_rope, rope_args), (ae.ae_prompt_attention, prompt_args),
+@pytest.mark.parametrize("kw,status", [
+    (dict(batch=-1), SHAPE), (dict(batch=65), SHAPE), (dict(n_axes=0), SHAPE), (dict(n_axes=5), SHAPE),
+    (dict(pair_axis=bytes([1] * 32)), INVALID), (dict(norm_offset=float("inf")), INVALID),
+    (dict(cu_lens=None), INVALID), (dict(cu=(0, 3, 2)), SHAPE), (dict(cu=(1, 2)), SHAPE), (dict(cu=(0, 2, 5)), SHAPE),
+    (dict(embeddings=None), INVALID), (dict(embeddings=FAKE + 4), INVALID), (dict(out_k=None), INVALID),
+    (dict(out_v=FAKE + 2), INVALID), (dict(positions=None), INVALID), (dict(positions=FAKE + 1), INVALID)])
+def test_prefill_prompts_refuses(make_context, kw, status):
+    refused(ae.ae_prefill_prompts, make_context(), prefill_args(**kw), status)
+
+
+@pytest.mark.parametrize("norm", [None, FAKE + 8])
+def test_prefill_prompts_refuses_norm_weights(make_context, norm):
+    arr = (ctypes.c_void_p * 1)(norm)
+    refused(ae.ae_prefill_prompts, make_context(), prefill_args(k_norm=ctypes.addressof(arr)), INVALID)
+
+
+@pytest.mark.parametrize("call,args", [(ae.ae_prefill_prompts, prefill_args), (ae.ae_qk_norm_rope, rope_args), (ae.ae_prompt_attention, prompt_args),
                                        (ae.ae_token_attention, token_args)])
 def test_fp32_contexts_and_null_are_refused(make_context, call, args):
     refused(call, make_context(bf16=0), args(), UNSUPPORTED)
@@ -135,4 +161,5 @@ def test_nothing_to_do_is_ok(make_context):
     ae.ae_qk_norm_rope(c, rope_args(tokens=0, qkv=None, q_out=None, k_cache=None, v_cache=None, positions=None))
     ae.ae_prompt_attention(c, prompt_args(cu=(0,), row0=None, lens=None, q=None, k=None, v=None, out=None))
     ae.ae_prompt_attention(c, prompt_args(cu=(0, 0, 0), row0=(0, 5), lens=(0, 3), q=None, k=None, v=None, out=None))
+    ae.ae_prefill_prompts(c, prefill_args(cu=(0, 0), embeddings=None, out_k=None, out_v=None, positions=None))
     ae.ae_token_attention(c, token_args(batch=0, q=None, k=None, v=None, out=None))
