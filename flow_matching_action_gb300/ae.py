@@ -242,23 +242,41 @@ def ae_prefill_prompts(ctx, args: ae_prefill_prompts_args) -> None:
     _check(lib().ae_prefill_prompts(ctx, ctypes.byref(args)), ctx)
 
 
+_dtypes = None
+
+
+def _torch_dtypes():
+    """(bf16, int32, int64, uint8): the module works without torch until tensors are passed."""
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        _dtypes = (torch.bfloat16, torch.int32, torch.int64, torch.uint8)
+    return _dtypes
+
+
+_BF16, _I32, _I64, _U8 = range(4)
+
+
 def _rows(name: str, t, width: int, rows: Optional[int] = None):
     """(pointer, row stride) of a bf16 CUDA tensor [rows, width] whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[1] != width or (rows is not None and t.shape[0] != rows):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [{'rows' if rows is None else rows}, {width}]")
-    if str(t.dtype) != "torch.bfloat16" or not t.is_cuda:
+    shape, dt = t.shape, _dtypes or _torch_dtypes()
+    if len(shape) != 2 or shape[1] != width or (rows is not None and shape[0] != rows):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [{'rows' if rows is None else rows}, {width}]")
+    if t.dtype is not dt[_BF16] or not t.is_cuda:
         raise ValueError(f"{name}: expected a bf16 CUDA tensor, got {t.dtype} on {t.device}")
-    if width > 1 and t.stride(1) != 1:
+    step = t.stride()
+    if step[1] != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width  # one row has no stride
+    return t.data_ptr(), step[0] if shape[0] > 1 else width  # one row has no stride
 
 
-def _vec(name: str, t, dtype: str, n: int):
+def _vec(name: str, t, dtype: int, n: int):
     """Pointer of a contiguous CUDA tensor of n elements, or None."""
     if t is None:
         return None
-    if str(t.dtype) != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
-        raise ValueError(f"{name}: expected {n} contiguous {dtype} elements on the GPU, got {tuple(t.shape)} "
+    want = (_dtypes or _torch_dtypes())[dtype]
+    if t.dtype is not want or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name}: expected {n} contiguous {want} elements on the GPU, got {tuple(t.shape)} "
                          f"{t.dtype} on {t.device}")
     return t.data_ptr()
 
@@ -343,6 +361,7 @@ class ActionExpert:
         self.dims = dims
         self.config = make_config(dims, dtype, fp8_weights)
         self._wstruct = make_weights(weights)
+        self._q_dim, self._kv_dim = dims.n_q_heads * dims.head_dim, dims.n_kv_heads * dims.head_dim
         self.ctx = ae_create(self.config, self._wstruct, max_batch, max_prefix_rows, stream)
         self._bound = None
 
@@ -369,58 +388,48 @@ class ActionExpert:
         positions int32 [tokens] or [axes, tokens]; kv_rows int64 [tokens] or None; pair_axis bytes or a
         sequence of dh / 2 axes; pair_freq a sequence of dh / 2 frequencies.
         """
-        d = self.dims
-        n = qkv.shape[0]
-        a = ae_qk_norm_rope_args()
-        a.tokens = n
-        a.n_axes = positions.shape[0] if positions.dim() == 2 else 1
-        a.qkv, a.qkv_stride = _rows("qkv", qkv, d.q_dim + 2 * d.kv_dim)
-        a.q_norm = _vec("q_norm", q_norm, "torch.bfloat16", d.head_dim)
-        a.k_norm = _vec("k_norm", k_norm, "torch.bfloat16", d.head_dim)
-        a.norm_offset = norm_offset
-        a.positions = _vec("positions", positions, "torch.int32", a.n_axes * n)
-        a.pair_axis, freq = _pairs(pair_axis, pair_freq, d.head_dim // 2)
-        a.pair_freq = _addr(freq)
-        a.kv_rows = _vec("kv_rows", kv_rows, "torch.int64", n)
-        a.q_out, a.q_stride = _rows("q_out", q_out, d.q_dim, n)
-        a.k_cache, a.kv_stride = _rows("k_cache", k_cache, d.kv_dim)
-        a.cache_rows = k_cache.shape[0]
-        a.v_cache, v_stride = _rows("v_cache", v_cache, d.kv_dim, k_cache.shape[0])
-        if v_stride != a.kv_stride:
+        qd, kvd, dh = self._q_dim, self._kv_dim, self.dims.head_dim
+        n, cache_rows = qkv.shape[0], k_cache.shape[0]
+        axes = positions.shape[0] if positions.dim() == 2 else 1
+        pair_axis, freq = _pairs(pair_axis, pair_freq, dh // 2)
+        x, x_stride = _rows("qkv", qkv, qd + 2 * kvd)
+        q, q_stride = _rows("q_out", q_out, qd, n)
+        k, k_stride = _rows("k_cache", k_cache, kvd)
+        v, v_stride = _rows("v_cache", v_cache, kvd, cache_rows)
+        if v_stride != k_stride:
             raise ValueError("k_cache and v_cache have different row strides")
-        ae_qk_norm_rope(self.ctx, a)
+        ae_qk_norm_rope(self.ctx, ae_qk_norm_rope_args(
+            n, axes, x, x_stride, _vec("q_norm", q_norm, _BF16, dh), _vec("k_norm", k_norm, _BF16, dh), norm_offset,
+            _vec("positions", positions, _I32, axes * n), pair_axis, _addr(freq), _vec("kv_rows", kv_rows, _I64, n),
+            cache_rows, q, q_stride, k, v, k_stride))
 
     def prompt_attention(self, q, k, v, cu_q, kv_row0=None, kv_len=None, key_mask=None, causal: bool = True,
                          scale: float = 0.0, out=None):
         """Attention of packed prompts (see include/ae.h); returns out [rows, Hq dh].
 
         q [rows, Hq dh], k / v [cache rows, Hkv dh]: bf16.  cu_q, kv_row0, kv_len are host sequences;
-        key_mask uint8 [cache rows] on the GPU.
+        key_mask uint8 [cache rows] on the GPU.  Rows of out behind the last sequence are not written.
         """
-        d = self.dims
         if out is None:
-            out = q.new_zeros(q.shape)
-        a = ae_prompt_attention_args()
+            out = q.new_empty(q.shape)
         cu = _host_array(ctypes.c_int32, cu_q)
         row0, lens = _host_array(ctypes.c_int64, kv_row0), _host_array(ctypes.c_int32, kv_len)
-        a.batch = len(cu) - 1
+        batch = len(cu) - 1
         for name, x in (("kv_row0", row0), ("kv_len", lens)):
-            if x is not None and len(x) != a.batch:
-                raise ValueError(f"{name}: {len(x)} entries for {a.batch} sequences")
-        if q.shape[0] < cu[a.batch]:
-            raise ValueError(f"q: {q.shape[0]} rows, cu_q ends at {cu[a.batch]}")
-        a.causal = 1 if causal else 0
-        a.cu_q, a.kv_row0, a.kv_len = _addr(cu), _addr(row0), _addr(lens)
-        a.q, a.q_stride = _rows("q", q, d.q_dim)
-        a.k, a.kv_stride = _rows("k", k, d.kv_dim)
-        a.cache_rows = k.shape[0]
-        a.v, v_stride = _rows("v", v, d.kv_dim, k.shape[0])
-        if v_stride != a.kv_stride:
+            if x is not None and len(x) != batch:
+                raise ValueError(f"{name}: {len(x)} entries for {batch} sequences")
+        rows, cache_rows = q.shape[0], k.shape[0]
+        if rows < cu[batch]:
+            raise ValueError(f"q: {rows} rows, cu_q ends at {cu[batch]}")
+        qp, q_stride = _rows("q", q, self._q_dim)
+        kp, k_stride = _rows("k", k, self._kv_dim)
+        vp, v_stride = _rows("v", v, self._kv_dim, cache_rows)
+        if v_stride != k_stride:
             raise ValueError("k and v have different row strides")
-        a.key_mask = _vec("key_mask", key_mask, "torch.uint8", a.cache_rows)
-        a.scale = scale
-        a.out, a.out_stride = _rows("out", out, d.q_dim, q.shape[0])
-        ae_prompt_attention(self.ctx, a)
+        op, o_stride = _rows("out", out, self._q_dim, rows)
+        ae_prompt_attention(self.ctx, ae_prompt_attention_args(
+            batch, 1 if causal else 0, _addr(cu), _addr(row0), _addr(lens), cache_rows, qp, q_stride, kp, vp, k_stride,
+            _vec("key_mask", key_mask, _U8, cache_rows), scale, op, o_stride))
         return out
 
     def token_attention(self, q, k, v, kv_row0, kv_len, max_len: int, key_mask=None, scale: float = 0.0, out=None):
@@ -429,24 +438,18 @@ class ActionExpert:
         q [requests, Hq dh], k / v [cache rows, Hkv dh]: bf16; kv_row0 int64, kv_len int32 [requests] and
         key_mask uint8 [cache rows] on the GPU.
         """
-        d = self.dims
-        n = q.shape[0]
         if out is None:
             out = q.new_empty(q.shape)
-        a = ae_token_attention_args()
-        a.batch, a.max_len = n, max_len
-        a.kv_row0 = _vec("kv_row0", kv_row0, "torch.int64", n)
-        a.kv_len = _vec("kv_len", kv_len, "torch.int32", n)
-        a.q, a.q_stride = _rows("q", q, d.q_dim)
-        a.k, a.kv_stride = _rows("k", k, d.kv_dim)
-        a.cache_rows = k.shape[0]
-        a.v, v_stride = _rows("v", v, d.kv_dim, k.shape[0])
-        if v_stride != a.kv_stride:
+        n, cache_rows = q.shape[0], k.shape[0]
+        qp, q_stride = _rows("q", q, self._q_dim)
+        kp, k_stride = _rows("k", k, self._kv_dim)
+        vp, v_stride = _rows("v", v, self._kv_dim, cache_rows)
+        if v_stride != k_stride:
             raise ValueError("k and v have different row strides")
-        a.key_mask = _vec("key_mask", key_mask, "torch.uint8", a.cache_rows)
-        a.scale = scale
-        a.out, a.out_stride = _rows("out", out, d.q_dim, n)
-        ae_token_attention(self.ctx, a)
+        op, o_stride = _rows("out", out, self._q_dim, n)
+        ae_token_attention(self.ctx, ae_token_attention_args(
+            n, max_len, _vec("kv_row0", kv_row0, _I64, n), _vec("kv_len", kv_len, _I32, n), cache_rows, qp, q_stride,
+            kp, vp, k_stride, _vec("key_mask", key_mask, _U8, cache_rows), scale, op, o_stride))
         return out
 
     def prefill_prompts(self, embeddings, cu_lens, positions, out_k, out_v, causal: bool = True, token_mask=None,
@@ -463,10 +466,10 @@ class ActionExpert:
             raise ValueError(f"embeddings: {n} rows, cu_lens ends at {cu[len(cu) - 1]}")
         a = ae_prefill_prompts_args()
         a.batch, a.causal, a.cu_lens = len(cu) - 1, 1 if causal else 0, _addr(cu)
-        a.embeddings = _vec("embeddings", embeddings, "torch.bfloat16", n * d.width)
-        a.token_mask = _vec("token_mask", token_mask, "torch.uint8", n)
+        a.embeddings = _vec("embeddings", embeddings, _BF16, n * d.width)
+        a.token_mask = _vec("token_mask", token_mask, _U8, n)
         a.n_axes = positions.shape[0] if positions.dim() == 2 else 1
-        a.positions = _vec("positions", positions, "torch.int32", a.n_axes * n)
+        a.positions = _vec("positions", positions, _I32, a.n_axes * n)
         a.pair_axis, freq = _pairs(pair_axis, pair_freq, d.head_dim // 2)
         a.pair_freq = _addr(freq)
         norms = []
@@ -474,11 +477,11 @@ class ActionExpert:
             if w is not None and len(w) != d.layers:
                 raise ValueError(f"{name}: {len(w)} tensors for {d.layers} layers")
             norms.append(None if w is None else (ctypes.c_void_p * d.layers)(
-                *[_vec(name, x, "torch.bfloat16", d.head_dim) for x in w]))
+                *[_vec(name, x, _BF16, d.head_dim) for x in w]))
         a.q_norm, a.k_norm = _addr(norms[0]), _addr(norms[1])
         a.norm_offset = norm_offset
-        a.out_k = _vec("out_k", out_k, "torch.bfloat16", d.layers * n * d.kv_dim)
-        a.out_v = _vec("out_v", out_v, "torch.bfloat16", d.layers * n * d.kv_dim)
+        a.out_k = _vec("out_k", out_k, _BF16, d.layers * n * d.kv_dim)
+        a.out_v = _vec("out_v", out_v, _BF16, d.layers * n * d.kv_dim)
         ae_prefill_prompts(self.ctx, a)
 
     def sample(self, noise, n_steps: int, out=None):

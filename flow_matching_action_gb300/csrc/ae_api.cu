@@ -285,6 +285,10 @@ ae_status alloc_scratch(ae_ctx* c) {
   AE_TRY(alloc(c, &c->n_valid, (size_t)c->max_batch * sizeof(int)));
   AE_TRY(alloc(c, &c->rope_cs, (size_t)c->max_batch * d.H * (d.dh / 2) * sizeof(float2)));
   if (c->fast) {
+    uint64_t turn[128] = {0};
+    for (int j = 0; j < d.dh / 2; ++j) turn[j] = ae::turn_fraction(pow(d.theta, -2.0 * j / d.dh));
+    AE_TRY(alloc(c, &c->rope_turn, sizeof(turn)));
+    AE_CK(c, cudaMemcpyAsync(c->rope_turn, turn, sizeof(turn), cudaMemcpyHostToDevice, c->stream));
     AE_TRY(alloc(c, &c->sumsq, (size_t)(d.D / 128) * M * sizeof(float)));
     const size_t units = ae::attn_part_units(c->max_batch, d.H, d.Hq, d.Hkv, c->max_rows, c->sm_count);
     AE_TRY(alloc(c, &c->attn_o, units * 128 * d.dh * sizeof(float)));
@@ -505,8 +509,6 @@ ae_status ae_create(const ae_config* cfg, const ae_weights* w, int max_batch,
   c->d = Dims{cfg->layers, cfg->width, cfg->mlp, cfg->n_q_heads, cfg->n_kv_heads, cfg->head_dim,
               cfg->action_dim, cfg->horizon, cfg->rms_eps, cfg->rope_theta,
               cfg->time_min_period, cfg->time_max_period, cfg->dtype, cfg->ctx_dim};
-  for (int j = 0; j < c->d.dh / 2; ++j)
-    c->rope_turn[j] = ae::turn_fraction(pow(c->d.theta, -2.0 * j / c->d.dh));
   c->max_batch = max_batch;
   c->max_rows = max_prefix_rows;
   c->stream = (cudaStream_t)stream;

@@ -115,7 +115,7 @@ struct ae_ctx {
   ae::BindState bind;
 
   std::vector<ae::TimeTable> tables;
-  uint64_t rope_turn[128] = {0};  // rope_theta^(-2j/dh) per position as a fraction of a turn (ae_qk_norm_rope)
+  uint64_t* rope_turn = nullptr;  // [dh/2] rope_theta^(-2j/dh) per position as a fraction of a turn (ae_qk_norm_rope)
 
   // Sticky device status: host-mapped so it can be read without a sync.
   int* status_host = nullptr;
@@ -358,6 +358,7 @@ struct RopeNormArgs {
   bf16 *k_cache, *v_cache;
   int64_t kv_stride;
   int* status;
+  const uint64_t* turn_table;  // device copy of `turn` (the default ladder), or nullptr
   uint64_t turn[128];  // pair_freq / 2 pi as a fraction of a turn, in units of 2^-64
   uint8_t axis[128];
 };

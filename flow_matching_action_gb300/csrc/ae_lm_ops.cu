@@ -66,9 +66,10 @@ ae_status check_rotation(ae_ctx* c, int n_axes, const uint8_t* pair_axis, const 
 }
 
 void set_rotation(const ae_ctx* c, ae::RopeNormArgs* a, const uint8_t* pair_axis, const double* pair_freq) {
+  a->turn_table = pair_freq ? nullptr : c->rope_turn;
   for (int j = 0; j < c->d.dh / 2; ++j) {
     a->axis[j] = pair_axis ? pair_axis[j] : 0;
-    a->turn[j] = pair_freq ? ae::turn_fraction(pair_freq[j]) : c->rope_turn[j];
+    a->turn[j] = pair_freq ? ae::turn_fraction(pair_freq[j]) : 0;
   }
 }
 

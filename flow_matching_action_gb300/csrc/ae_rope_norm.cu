@@ -4,9 +4,10 @@
 // DH / 16 lanes hold one head: lane l has dims 8l .. 8l+7 and their rotation
 // partners DH/2 + 8l .. +7 (two 16-byte loads, every pair within a thread), so
 // a head's sum of squares is one shuffle reduction over its lanes and nothing
-// is exchanged for the rotation.  The angle's cosine and sine are computed once
-// per (token, pair) of the block and shared by the token's heads through
-// shared memory.
+// is exchanged for the rotation.  A warp works alone on a token (or on a part of
+// its heads when tokens are few): its lanes compute the token's cosines and
+// sines once, share them through the warp's slice of shared memory, and stream
+// the heads with the loads two steps ahead; no barrier between warps.
 // An angle is positions * frequency modulo one turn: the frequency as a 64-bit
 // fraction of a turn times the integer position wraps modulo 2^64, which is
 // the reduction, exact for every int32 position; its top 32 bits leave an
@@ -18,122 +19,203 @@ namespace ae {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBlocks = 3;  // resident a SM
 
-struct Vec8 {
-  uint4 u;
-};
-
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+// Two fp32 lanes of one 64-bit register (packed multiply-adds).
+typedef uint64_t f2;
+__device__ __forceinline__ f2 pair(float a, float b) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void split(f2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+// Eight bf16 as four pairs of fp32.
+__device__ __forceinline__ void unpack8(const uint4& u, f2 (&x)[4]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint4 pack8(const f2 (&x)[4]) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    float a, b;
+    split(x[i], a, b);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Eight fp32 of shared memory as four pairs.
+__device__ __forceinline__ void load8(const float* p, f2 (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float4 v = reinterpret_cast<const float4*>(p)[i];
+    x[2 * i] = pair(v.x, v.y);
+    x[2 * i + 1] = pair(v.z, v.w);
+  }
+}
+
 template <int DH>
-__global__ void __launch_bounds__(kThreads) k_qk_norm_rope(const __grid_constant__ RopeNormArgs a, int toks_per_block) {
+__global__ void __launch_bounds__(kThreads, kBlocks)
+    k_qk_norm_rope(const __grid_constant__ RopeNormArgs a, int parts) {
   constexpr int HALF = DH / 2;
   constexpr int LPH = DH / 16;       // lanes of a head
   constexpr int HPW = 32 / LPH;      // heads a warp works on at once
-  extern __shared__ float2 cs[];     // [toks_per_block][HALF] (cos, sin)
-  const int tok0 = blockIdx.x * toks_per_block;
-  const int ntok = min(toks_per_block, a.tokens - tok0);
-  for (int i = threadIdx.x; i < ntok * HALF; i += kThreads) {
-    const int t = i / HALF, j = i - t * HALF;
-    const int64_t pos = a.positions[(int64_t)a.axis[j] * a.tokens + tok0 + t];
-    const int32_t frac = (int32_t)(uint32_t)(((uint64_t)pos * a.turn[j]) >> 32);  // in [-1/2, 1/2) turns
-    float s, c;
-    sincospif((float)frac * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-    cs[i] = make_float2(c, s);
-  }
-  __syncthreads();
+  constexpr int PAIRS = HALF / 32;   // rotation pairs whose angles a lane computes
+  __shared__ __align__(16) float trig_all[kThreads / 32][3][HALF];  // cos, sin, -sin of the warp's token
+  __shared__ __align__(16) float norm_w[2][DH];                     // norm_offset + w of queries, keys
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = lane / LPH, l = lane % LPH;
-  const int heads = a.Hq + 2 * a.Hkv;
-  const int units = ntok * heads;
-  for (int u0 = warp * HPW; u0 < units; u0 += (kThreads / 32) * HPW) {  // uniform for the warp
-    const int u = u0 + sub;
-    const bool on = u < units;
-    const int t = on ? u / heads : 0, h = on ? u - t * heads : 0;
-    const bf16* src = a.qkv + (int64_t)(tok0 + t) * a.qkv_stride + (int64_t)h * DH + 8 * l;
-    uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-    if (on) {
-      lo = *reinterpret_cast<const uint4*>(src);
-      hi = *reinterpret_cast<const uint4*>(src + HALF);
+  const int heads = a.Hq + 2 * a.Hkv, n_rot = a.Hq + a.Hkv;
+  float(*trig)[HALF] = trig_all[warp];
+  const int items = a.tokens * parts, stride = gridDim.x * (kThreads / 32);
+  int item = blockIdx.x * (kThreads / 32) + warp;
+
+  auto fetch = [&](int t, int h, uint4& lo, uint4& hi) {
+    if (h >= heads) return;
+    const bf16* src = a.qkv + (int64_t)t * a.qkv_stride + (int64_t)h * DH + 8 * l;
+    lo = *reinterpret_cast<const uint4*>(src);
+    hi = *reinterpret_cast<const uint4*>(src + HALF);
+  };
+  int t = item / parts, h0 = (item - t * parts) * HPW;
+  uint4 lo1 = make_uint4(0, 0, 0, 0), hi1 = lo1;  // the next step's pieces
+  if (item < items) fetch(t, h0 + sub, lo1, hi1);
+
+  // the lane's pairs, the same for every token: read once (the argument's
+  // entries are constants, which lanes at different addresses read one by one)
+  uint64_t turn[PAIRS];
+  int axis[PAIRS], pos[PAIRS];
+  int64_t row = 0;
+#pragma unroll
+  for (int i = 0; i < PAIRS; ++i) {
+    turn[i] = a.turn_table ? a.turn_table[lane + 32 * i] : a.turn[lane + 32 * i];
+    axis[i] = a.n_axes > 1 ? a.axis[lane + 32 * i] * a.tokens : 0;
+    pos[i] = item < items ? a.positions[(int64_t)axis[i] + t] : 0;
+  }
+  if (item < items) row = a.kv_rows ? a.kv_rows[t] : t;
+  if (a.q_norm != nullptr || a.k_norm != nullptr)
+    for (int i = threadIdx.x; i < DH; i += kThreads) {
+      norm_w[0][i] = a.q_norm ? a.norm_offset + __bfloat162float(a.q_norm[i]) : 0.f;
+      norm_w[1][i] = a.k_norm ? a.norm_offset + __bfloat162float(a.k_norm[i]) : 0.f;
     }
-    bf16* dst = nullptr;
-    if (on && h < a.Hq) {
-      dst = a.q_out + (int64_t)(tok0 + t) * a.q_stride + (int64_t)h * DH;
-    } else if (on) {
-      const int64_t row = a.kv_rows ? a.kv_rows[tok0 + t] : tok0 + t;
-      if (row >= a.cache_rows) {
-        tc::report(a.status, kDevBounds);
-      } else if (row >= 0) {
-        const int kh = h - a.Hq;
-        dst = (kh < a.Hkv ? a.k_cache + row * a.kv_stride + (int64_t)kh * DH
-                          : a.v_cache + row * a.kv_stride + (int64_t)(kh - a.Hkv) * DH);
-      }
+  __syncthreads();
+
+  while (item < items) {  // uniform for the warp
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      const int32_t frac = (int32_t)(uint32_t)(((uint64_t)(int64_t)pos[i] * turn[i]) >> 32);  // in [-1/2, 1/2) turns
+      float sn, cn;
+      sincospif((float)frac * 4.656612873077393e-10f, &sn, &cn);  // 2^-31: half turns
+      trig[0][lane + 32 * i] = cn;
+      trig[1][lane + 32 * i] = sn;
+      trig[2][lane + 32 * i] = -sn;
     }
-    float x[8], y[8];
-    unpack8(lo, x);
-    unpack8(hi, y);
-    const bf16* w = h < a.Hq ? a.q_norm : a.k_norm;
-    float ss = 0.f;
+    __syncwarp();
+    const int64_t tok = t, dst_row = row;
+    item += stride;
+    const int t1 = item / parts, h1 = (item - t1 * parts) * HPW;
+    if (item < items) {  // the next token's positions and cache row
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += x[i] * x[i] + y[i] * y[i];
+      for (int i = 0; i < PAIRS; ++i) pos[i] = a.positions[(int64_t)axis[i] + t1];
+      row = a.kv_rows ? a.kv_rows[t1] : t1;
+    }
+    bf16* q_row = a.q_out + tok * a.q_stride + 8 * l;
+    const bool store_kv = dst_row >= 0 && dst_row < a.cache_rows;
+    if (dst_row >= a.cache_rows) tc::report(a.status, kDevBounds);
+    for (; h0 < heads; h0 += parts * HPW) {
+      uint4 lo = lo1, hi = hi1;
+      const int hn = h0 + parts * HPW;
+      if (hn < heads) fetch((int)tok, hn + sub, lo1, hi1);
+      else if (item < items) fetch(t1, h1 + sub, lo1, hi1);
+      const int h = h0 + sub;
+      f2 x[4], y[4];
+      unpack8(lo, x);
+      unpack8(hi, y);
+      if (h0 < n_rot) {  // a step of values only skips the arithmetic
+        f2 s2 = 0;
 #pragma unroll
-    for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (h < a.Hq + a.Hkv && on) {
-      if (w != nullptr) {
-        const float r = rsqrtf(ss * (1.f / DH) + a.eps);
-        float wl[8], wh[8];
-        unpack8(*reinterpret_cast<const uint4*>(w + 8 * l), wl);
-        unpack8(*reinterpret_cast<const uint4*>(w + HALF + 8 * l), wh);
+        for (int i = 0; i < 4; ++i) s2 = fma2(y[i], y[i], fma2(x[i], x[i], s2));
+        float ss, se;
+        split(s2, ss, se);
+        ss += se;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] *= r * (a.norm_offset + wl[i]);
-          y[i] *= r * (a.norm_offset + wh[i]);
+        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (h < n_rot) {
+          const bool is_k = h >= a.Hq;
+          if ((is_k ? a.k_norm : a.q_norm) != nullptr) {
+            const float r = rsqrtf(ss * (1.f / DH) + a.eps);
+            const f2 r2 = pair(r, r);
+            f2 wl[4], wh[4];
+            load8(norm_w[is_k] + 8 * l, wl);
+            load8(norm_w[is_k] + HALF + 8 * l, wh);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              x[i] = mul2(x[i], mul2(r2, wl[i]));
+              y[i] = mul2(y[i], mul2(r2, wh[i]));
+            }
+          }
+          f2 c[4], sn[4], ns[4];
+          load8(trig[0] + 8 * l, c);
+          load8(trig[1] + 8 * l, sn);
+          load8(trig[2] + 8 * l, ns);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f2 p = fma2(y[i], ns[i], mul2(x[i], c[i]));
+            y[i] = fma2(x[i], sn[i], mul2(y[i], c[i]));
+            x[i] = p;
+          }
+          lo = pack8(x);
+          hi = pack8(y);
         }
       }
-      const float2* c = cs + t * HALF + 8 * l;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 z = c[i];
-        const float p = x[i] * z.x - y[i] * z.y;
-        y[i] = y[i] * z.x + x[i] * z.y;
-        x[i] = p;
+      bf16* dst = nullptr;
+      if (h < a.Hq) dst = q_row + (int64_t)h * DH;
+      else if (h < heads && store_kv)
+        dst = (h < n_rot ? a.k_cache + (int64_t)(h - a.Hq) * DH : a.v_cache + (int64_t)(h - n_rot) * DH) +
+              dst_row * a.kv_stride + 8 * l;
+      if (dst != nullptr) {
+        *reinterpret_cast<uint4*>(dst) = lo;
+        *reinterpret_cast<uint4*>(dst + HALF) = hi;
       }
-      lo = pack8(x);
-      hi = pack8(y);
     }
-    if (dst != nullptr) {
-      *reinterpret_cast<uint4*>(dst + 8 * l) = lo;
-      *reinterpret_cast<uint4*>(dst + HALF + 8 * l) = hi;
-    }
+    t = t1;
+    h0 = h1;
   }
+}
+
+template <int DH>
+cudaError_t launch(const RopeNormArgs& a, int sm_count, cudaStream_t s) {
+  constexpr int HPW = 512 / DH, W = kThreads / 32;
+  // tokens that do not fill the GPU's warps are split by heads
+  const int warps = kBlocks * W * sm_count, steps = (a.Hq + 2 * a.Hkv + HPW - 1) / HPW;
+  int parts = warps / a.tokens;
+  parts = parts < 1 ? 1 : (parts > steps ? steps : parts);
+  const int64_t blocks = ((int64_t)a.tokens * parts + W - 1) / W;
+  const unsigned grid = (unsigned)(blocks < kBlocks * sm_count ? blocks : kBlocks * sm_count);
+  return launch_k(k_qk_norm_rope<DH>, dim3(grid), dim3(kThreads), 0, s, false, a, parts);
 }
 
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const RopeNormArgs& a, int dh, int sm_count, cudaStream_t s) {
-  const int tpb = a.tokens >= 8 * sm_count ? 4 : 1;
-  const int grid = (a.tokens + tpb - 1) / tpb;
-  const size_t smem = (size_t)tpb * (dh / 2) * sizeof(float2);
-  if (dh == 64) return launch_k(k_qk_norm_rope<64>, dim3(grid), dim3(kThreads), smem, s, false, a, tpb);
-  if (dh == 128) return launch_k(k_qk_norm_rope<128>, dim3(grid), dim3(kThreads), smem, s, false, a, tpb);
-  return launch_k(k_qk_norm_rope<256>, dim3(grid), dim3(kThreads), smem, s, false, a, tpb);
+  if (dh == 64) return launch<64>(a, sm_count, s);
+  if (dh == 128) return launch<128>(a, sm_count, s);
+  return launch<256>(a, sm_count, s);
 }
 
 }  // namespace ae
