@@ -37,6 +37,14 @@ __device__ __forceinline__ void report(int* status, int code) {
   if (status != nullptr) *(volatile int*)status = code;
 }
 
+// One lane of a converged warp, chosen so that the compiler knows the branch to
+// be uniform: MMA operands then stay in uniform registers.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- mbarrier
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(count) : "memory");
