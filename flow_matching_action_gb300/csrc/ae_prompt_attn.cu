@@ -34,6 +34,7 @@ namespace {
 
 using namespace tc;
 
+constexpr int kListTiles = 512;
 constexpr float kRaise = 8.f;  // log2: raise the exponent reference past this
 
 template <int DH>
@@ -53,7 +54,8 @@ struct Cfg {
   static constexpr int BARS = RING + NS * SLOT;
   static constexpr int ML = NQ * 128 * DH * 4;     // a split's partial: fp32 rows, then [NQ][128] (m, l)
   static constexpr int WT = ML + NQ * 128 * 8;     // [rows of this CTA][split] weights of the merge
-  static constexpr int BYTES = BARS + 256 + 1024;
+  static constexpr int LIST = BARS + 256;          // key tiles with valid keys (masked calls): entries, then states
+  static constexpr int BYTES = LIST + kListTiles * 3 + 1024;
   // tensor memory columns
   static constexpr int O0 = 256;
   static_assert(WT + NQ * 128 * 4 <= BARS, "fp32 partials fit over the tiles");
@@ -72,9 +74,15 @@ struct Bars {
   uint64_t q, full[8], empty[8], s[2], p[2], o[2], drain;
   uint32_t tmem;
   int abort;
+  int listed[2];  // listed tiles of each query tile
 };
 static_assert(sizeof(Bars) <= 256, "");
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -208,7 +216,8 @@ __device__ __forceinline__ Unit find_unit(const PromptAttnArgs& a, const Launch&
   return w;
 }
 
-template <int DH>
+// MASKED: the call has a key mask.
+template <int DH, bool MASKED>
 __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     k_prompt_attn(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PromptAttnArgs a,
@@ -222,7 +231,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = L.split > 1 ? (int)cluster_rank() : 0;
   const Unit w = find_unit<DH>(a, L, blockIdx.x / L.split);
-  const uint8_t* mask = a.key_mask ? a.key_mask + w.kv_row0 : nullptr;
+  const uint8_t* mask = MASKED ? a.key_mask + w.kv_row0 : nullptr;
 
   // key tiles of every query tile: up to its last token's last key
   int cnt[NQ], most = 0;
@@ -242,20 +251,6 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     n_tiles = max(n_tiles, cnt[s]);
   }
 
-  // The load warp sets the barriers up and starts the first copies at once;
-  // the other warps meet it behind them.  The ring holds the tiles in the order
-  // the MMAs use them: K0 V0 K1 V1 .. (NQ = 2), K0 K1 V0 K2 V1 .. (NQ = 1).
-  int loaded = 0;
-  auto load = [&]() {
-    const int i = loaded;
-    const bool is_v = NQ == 2 ? (i & 1) : (i > 0 && ((i & 1) == 0 || i + 1 == 2 * n_tiles));
-    const int t = NQ == 2 ? i >> 1 : (is_v ? (i + 1 == 2 * n_tiles ? n_tiles - 1 : (i >> 1) - 1) : (i + 1) >> 1);
-    const int slot = i % NS;
-    mbar_arrive_expect_tx(&B->full[slot], C::SLOT);
-    tma_load_3d_nohint(smem + C::RING + slot * C::SLOT, is_v ? &vmap : &kmap, &B->full[slot], 0,
-                       (int)(w.kv_row0 + (int64_t)(lo + t) * BK), w.kvh * DB);
-    ++loaded;
-  };
   if (warp == C::W_LOAD && lane == 0) {
     mbar_init(&B->q, 1);
     mbar_init(&B->drain, 1);
@@ -271,20 +266,75 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
-    if (n_tiles > 0) {
-      mbar_arrive_expect_tx(&B->q, (uint32_t)(NQ * DB * L.T * L.Gc * 128));
-#pragma unroll
-      for (int s = 0; s < NQ; ++s)
-#pragma unroll
-        for (int d = 0; d < DB; ++d)
-          tma_load_3d_nohint(smem + s * C::QBYTES + d * (128 * 128), &qmap, &B->q, d * 64, w.kvh * L.G + w.g0,
-                             w.q_row0 + w.tok0 + s * L.T);
-      while (loaded < NS && loaded < 2 * n_tiles) load();
-    }
   }
   if (warp == C::W_MMA) {
     tmem_alloc(&B->tmem, 512);
     tmem_relinquish();
+  }
+  // Masked calls: the tiles that hold a valid key, in order, with the top bit
+  // set when some of their keys are masked; all other tiles are skipped.  (Key
+  // ranges beyond the list's room look every tile's mask up instead.)
+  uint16_t* list = reinterpret_cast<uint16_t*>(smem + C::LIST);
+  const bool listed = MASKED && n_tiles <= kListTiles;
+  if (listed) {
+    uint8_t* state = smem + C::LIST + kListTiles * 2;  // 0 none, 1 some, 2 all keys valid
+    for (int t = warp; t < n_tiles; t += C::THREADS / 32) {
+      uint32_t bits[BK / 32], any = 0, all = 0xffffffffu;
+      tile_bits<BK>(mask, (lo + t) * BK, w.n_keys, bits);
+#pragma unroll
+      for (int k = 0; k < BK / 32; ++k) {
+        any |= bits[k];
+        all &= bits[k];
+      }
+      if (lane == 0) state[t] = any == 0 ? 0 : (all == 0xffffffffu ? 2 : 1);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      int n = 0, first = 0;  // listed tiles; those of the first query tile
+      for (int t0 = 0; t0 < n_tiles; t0 += 32) {
+        const int t = t0 + lane, st = t < n_tiles ? state[t] : 0;
+        const uint32_t m = __ballot_sync(0xffffffffu, st != 0);
+        if (st != 0) list[n + __popc(m & ((1u << lane) - 1u))] = (uint16_t)(t | (st == 1 ? 0x8000 : 0));
+        n += __popc(m);
+        first += __popc(m & low_bits(cnt[0] - t0, 0));
+      }
+      if (lane == 0) {
+        B->listed[0] = first;
+        B->listed[NQ - 1] = NQ == 1 ? n : (cnt[NQ - 1] >= cnt[0] ? n : 0);
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < NQ; ++s) cnt[s] = B->listed[s];
+    n_tiles = max(cnt[0], cnt[NQ - 1]);
+  }
+  // key tile (from lo) of the i-th step, and whether some of its keys are masked
+  auto tile_at = [&](int i) { return listed ? list[i] & 0x7fff : i; };
+  auto holes_at = [&](int i) { return listed ? (list[i] & 0x8000) != 0 : MASKED; };
+
+  // The load warp starts the first copies before the CTA meets.  The ring holds
+  // the tiles in the order the MMAs use them: K0 V0 K1 V1 .. (NQ = 2),
+  // K0 K1 V0 K2 V1 .. (NQ = 1).
+  int loaded = 0;
+  auto load = [&]() {
+    const int i = loaded;
+    const bool is_v = NQ == 2 ? (i & 1) : (i > 0 && ((i & 1) == 0 || i + 1 == 2 * n_tiles));
+    const int t = NQ == 2 ? i >> 1 : (is_v ? (i + 1 == 2 * n_tiles ? n_tiles - 1 : (i >> 1) - 1) : (i + 1) >> 1);
+    const int slot = i % NS;
+    mbar_arrive_expect_tx(&B->full[slot], C::SLOT);
+    tma_load_3d_nohint(smem + C::RING + slot * C::SLOT, is_v ? &vmap : &kmap, &B->full[slot], 0,
+                       (int)(w.kv_row0 + (int64_t)(lo + tile_at(t)) * BK), w.kvh * DB);
+    ++loaded;
+  };
+  if (warp == C::W_LOAD && lane == 0 && n_tiles > 0) {
+    mbar_arrive_expect_tx(&B->q, (uint32_t)(NQ * DB * L.T * L.Gc * 128));
+#pragma unroll
+    for (int s = 0; s < NQ; ++s)
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+        tma_load_3d_nohint(smem + s * C::QBYTES + d * (128 * 128), &qmap, &B->q, d * 64, w.kvh * L.G + w.g0,
+                           w.q_row0 + w.tok0 + s * L.T);
+    while (loaded < NS && loaded < 2 * n_tiles) load();
   }
   tc_fence_before();
   __syncthreads();
@@ -343,10 +393,11 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     };
     // zero the V rows of tile i that no query may see
     auto clean_v = [&](int i, int slot) {
-      const int key0 = (lo + i) * BK;
-      if (mask == nullptr && key0 + BK <= w.n_keys) return;
+      const int key0 = (lo + tile_at(i)) * BK;
+      const bool holes = holes_at(i);
+      if (!holes && key0 + BK <= w.n_keys) return;
       uint32_t bits[BK / 32];
-      tile_bits<BK>(mask, key0, w.n_keys, bits);
+      tile_bits<BK>(holes ? mask : nullptr, key0, w.n_keys, bits);
       uint32_t all = 0xffffffffu;
 #pragma unroll
       for (int k = 0; k < BK / 32; ++k) all &= bits[k];
@@ -443,11 +494,11 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     for (int i = 0; i < n; ++i) {
       const int buf = NQ == 1 ? i & 1 : s;
       const uint32_t tm_s = tmem + lane_off + (uint32_t)(buf * BK);
-      const int key0 = (lo + i) * BK;
-      const bool partial = mask != nullptr || key0 + BK > open;
+      const int key0 = (lo + tile_at(i)) * BK;
+      const bool holes = holes_at(i), partial = holes || key0 + BK > open;
       uint32_t bits[BK / 32];
       if (partial) {
-        tile_bits<BK>(mask, key0, w.n_keys, bits);
+        tile_bits<BK>(holes ? mask : nullptr, key0, w.n_keys, bits);
 #pragma unroll
         for (int k = 0; k < BK / 32; ++k) bits[k] &= low_bits(limit - key0, k);
       }
@@ -460,19 +511,20 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
       float mx[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) mx[e] = -INFINITY;
-      tmem_ld32_start(tm_s, sc[0]);
 #pragma unroll
-      for (int k = 0; k < BK / 32; ++k) {  // the next 32 scores arrive under this maximum
-        tmem_ld_wait();
+      for (int k = 0; k < BK / 32; ++k) tmem_ld32_start(tm_s + 32 * k, sc[k]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int k = 0; k < BK / 32; ++k) {
         landed(sc[k]);
-        if (k + 1 < BK / 32) tmem_ld32_start(tm_s + 32 * (k + 1), sc[k + 1]);
         if (partial) {
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             if (!((bits[k] >> j) & 1u)) sc[k][j] = 0xff800000u;  // -inf
         }
 #pragma unroll
-        for (int j = 0; j < 32; ++j) mx[j & 7] = fmaxf(mx[j & 7], __uint_as_float(sc[k][j]));
+        for (int j = 0; j < 32; j += 2)
+          mx[(j >> 1) & 7] = max3(mx[(j >> 1) & 7], __uint_as_float(sc[k][j]), __uint_as_float(sc[k][j + 1]));
       }
       const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])),
                               fmaxf(fmaxf(mx[4], mx[5]), fmaxf(mx[6], mx[7]))) * c;
@@ -504,25 +556,23 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
       }
       const float base = m == -INFINITY ? 0.f : -m;
       const uint64_t c2 = pack2(c, c), b2 = pack2(base, base);
-      uint64_t sum[2] = {0, 0};
+      uint64_t sum[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        constexpr int HK = BK / 2;
-        uint32_t p[HK / 2];
+      for (int k = 0; k < BK / 32; ++k) {
+        uint32_t p[16];
 #pragma unroll
-        for (int j = 0; j < HK; j += 2) {
-          const int k = (h * HK + j) >> 5, e = (h * HK + j) & 31;
+        for (int e = 0; e < 32; e += 2) {
           float x, y;
           unpack2(fma2(pack2(__uint_as_float(sc[k][e]), __uint_as_float(sc[k][e + 1])), c2, b2), x, y);
           x = ex2_fast(x);
           y = ex2_fast(y);
-          sum[(j >> 1) & 1] = add2(sum[(j >> 1) & 1], pack2(x, y));
-          p[j >> 1] = bf16x2(x, y);
+          sum[(e >> 1) & 3] = add2(sum[(e >> 1) & 3], pack2(x, y));
+          p[e >> 1] = bf16x2(x, y);
         }
-        tmem_st(tm_s + (HK / 2) * h, p);  // over S columns read above
+        tmem_st(tm_s + 16 * k, p);  // over S columns read above
       }
       float x, y;
-      unpack2(add2(sum[0], sum[1]), x, y);
+      unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
       l += x + y;
       tmem_st_wait();
       tc_fence_before();
@@ -590,6 +640,11 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     __syncwarp();
     cluster_arrive();
     cluster_wait();
+    // the unit found again: kept in registers it would spill in the loops above
+    unsigned bx = blockIdx.x;
+    asm volatile("" : "+r"(bx));
+    const Unit w = find_unit<DH>(a, L, bx / L.split);
+    const int rank = (int)cluster_rank();
     // rank r merges its share of the rows: the weight 2^(m_p - m) / l of every
     // split first, then DH / 4 four-dim pieces a row, four pieces a thread at once
     const int share = NQ * 128 / L.split;
@@ -700,7 +755,8 @@ cudaError_t launch(const PromptAttnArgs& a, int sm_count, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = L.split > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, k_prompt_attn<DH>, qmap, kmap, vmap, a, L);
+  return a.key_mask ? cudaLaunchKernelEx(&cfg, k_prompt_attn<DH, true>, qmap, kmap, vmap, a, L)
+                    : cudaLaunchKernelEx(&cfg, k_prompt_attn<DH, false>, qmap, kmap, vmap, a, L);
 }
 
 }  // namespace
@@ -711,12 +767,19 @@ cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int dh, int sm_coun
   return launch<256>(a, sm_count, s);
 }
 
+template <int DH>
+static cudaError_t setup() {
+  cudaError_t e = cudaSuccess;
+  for (auto kern : {k_prompt_attn<DH, false>, k_prompt_attn<DH, true>})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DH>::BYTES);
+  return e;
+}
+
 cudaError_t prompt_kernel_setup() {
-  cudaError_t e = cudaFuncSetAttribute(k_prompt_attn<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<64>::BYTES);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_prompt_attn<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<128>::BYTES);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_prompt_attn<256>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<256>::BYTES);
+  cudaError_t e = setup<64>();
+  if (e == cudaSuccess) e = setup<128>();
+  if (e == cudaSuccess) e = setup<256>();
   return e;
 }
 

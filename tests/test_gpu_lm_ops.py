@@ -265,6 +265,13 @@ def test_prompt_attention_long(experts, hq, hkv, dh):
     run_prompt(experts(hq, hkv, dh), hq, hkv, dh, [9, 3], [4000, 3000], gap=5, seed=12)
 
 
+def test_prompt_attention_masked_key_ranges_of_any_length(experts):
+    """Masked caches whose share of a CTA is beyond the room of its tile list, and well within it."""
+    for dh, n in ((256, 300000), (64, 70000)):
+        run_prompt(experts(8, 1, 256) if dh == 256 else experts(4, 1, 64), 8 if dh == 256 else 4, 1, dh, [5], [n - 5],
+                   masked=lambda i, m: (i // 100) % 3 != 1 and i % 7 != 0, gap=1, seed=n)
+
+
 @pytest.mark.parametrize("std,scale", [(30.0, 0.0), (1.0, 3.0), (1e-3, 0.0), (1.0, 1e-4)])
 def test_prompt_attention_score_ranges(experts, std, scale):
     """Peaked and flat softmaxes (scores of several hundred, scores near zero)."""
