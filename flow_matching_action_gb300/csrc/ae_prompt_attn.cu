@@ -65,6 +65,8 @@ struct Cfg {
 struct Launch {
   int n_order;                       // sequences with work
   int G, Gc, hc, T;                  // heads of a group, of a tile; head chunks; tokens of a tile
+  int per;                           // units of one token range: KV heads x head chunks
+  uint32_t per_inv, gc_inv;          // ceil(2^32 / per), ceil(2^32 / Gc)
   int split;                         // CTAs of a cluster
   int work_cu[AE_MAX_BATCH + 1];     // first work unit of the i-th sequence, longest first
   uint8_t order[AE_MAX_BATCH];
@@ -193,24 +195,30 @@ struct Unit {
   int kvh, g0;     // KV head; first head of the tile within its group
 };
 
+// x / d for x >= 0; inv = ceil(2^32 / d) where x * d < 2^32 for every x (then
+// the high word of the product is exact), else 0.
+__device__ __forceinline__ int divide(int x, int d, uint32_t inv) {
+  return d == 1 ? x : (inv != 0u ? (int)__umulhi((uint32_t)x, inv) : x / d);
+}
+
 template <int DH>
 __device__ __forceinline__ Unit find_unit(const PromptAttnArgs& a, const Launch& L, int u) {
   int i = 0;
+  if (L.n_order > 1) {
 #pragma unroll
-  for (int step = 32; step > 0; step >>= 1)
-    if (i + step < L.n_order && L.work_cu[i + step] <= u) i += step;
+    for (int step = 32; step > 0; step >>= 1)
+      if (i + step < L.n_order && L.work_cu[i + step] <= u) i += step;
+  }
   const int b = L.order[i];
-  u -= L.work_cu[i];
+  // counted from the sequence's last unit: its longest key ranges come first
+  u = L.work_cu[i + 1] - 1 - u;
   Unit w;
   w.q_row0 = a.cu_q[b];
   w.n_new = a.cu_q[b + 1] - a.cu_q[b];
   w.n_keys = a.kv_len[b];
   w.kv_row0 = a.kv_row0[b];
-  const int per = a.Hkv * L.hc;
-  const int tiles = (w.n_new + L.T * Cfg<DH>::NQ - 1) / (L.T * Cfg<DH>::NQ);
-  const int t = tiles - 1 - u / per;  // longest key ranges first
-  const int h = u % per;
-  w.kvh = h / L.hc;
+  const int t = divide(u, L.per, L.per_inv), h = u - t * L.per;
+  w.kvh = L.hc == 1 ? h : h / L.hc;
   w.g0 = (h - w.kvh * L.hc) * L.Gc;
   w.tok0 = t * L.T * Cfg<DH>::NQ;
   return w;
@@ -220,7 +228,8 @@ __device__ __forceinline__ Unit find_unit(const PromptAttnArgs& a, const Launch&
 template <int DH, bool MASKED>
 __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     k_prompt_attn(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
-                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ PromptAttnArgs a,
+                  const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap,
+                  const __grid_constant__ PromptAttnArgs a,
                   const __grid_constant__ Launch L) {
   using C = Cfg<DH>;
   constexpr int NQ = C::NQ, BK = C::BK, DB = C::DB, NS = C::NS;
@@ -230,27 +239,6 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
   volatile int* abort_flag = &B->abort;
   const int warp = __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   const int rank = L.split > 1 ? (int)cluster_rank() : 0;
-  const Unit w = find_unit<DH>(a, L, blockIdx.x / L.split);
-  const uint8_t* mask = MASKED ? a.key_mask + w.kv_row0 : nullptr;
-
-  // key tiles of every query tile: up to its last token's last key
-  int cnt[NQ], most = 0;
-#pragma unroll
-  for (int s = 0; s < NQ; ++s) {
-    const int t0 = w.tok0 + s * L.T;
-    const int last = min(t0 + L.T, w.n_new) - 1;
-    const int keys = t0 >= w.n_new ? 0 : (a.causal ? w.n_keys - w.n_new + last + 1 : w.n_keys);
-    cnt[s] = (keys + BK - 1) / BK;
-    most = max(most, cnt[s]);
-  }
-  const int lo = (int)((int64_t)most * rank / L.split), hi = (int)((int64_t)most * (rank + 1) / L.split);
-  int n_tiles = 0;
-#pragma unroll
-  for (int s = 0; s < NQ; ++s) {
-    cnt[s] = max(0, min(cnt[s], hi) - lo);
-    n_tiles = max(n_tiles, cnt[s]);
-  }
-
   if (warp == C::W_LOAD && lane == 0) {
     mbar_init(&B->q, 1);
     mbar_init(&B->drain, 1);
@@ -266,11 +254,40 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
+    prefetch_tensormap(&qmap);
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+    prefetch_tensormap(&omap);
   }
   if (warp == C::W_MMA) {
     tmem_alloc(&B->tmem, 512);
     tmem_relinquish();
   }
+  const Unit w = find_unit<DH>(a, L, blockIdx.x / L.split);
+  const uint8_t* mask = MASKED ? a.key_mask + w.kv_row0 : nullptr;
+
+  // key tiles of every query tile: up to its last token's last key
+  int cnt[NQ], most = 0;
+#pragma unroll
+  for (int s = 0; s < NQ; ++s) {
+    const int t0 = w.tok0 + s * L.T;
+    const int last = min(t0 + L.T, w.n_new) - 1;
+    const int keys = t0 >= w.n_new ? 0 : (a.causal ? w.n_keys - w.n_new + last + 1 : w.n_keys);
+    cnt[s] = (keys + BK - 1) / BK;
+    most = max(most, cnt[s]);
+  }
+  int lo = 0, hi = most;
+  if (L.split > 1) {
+    lo = (int)((int64_t)most * rank / L.split);
+    hi = (int)((int64_t)most * (rank + 1) / L.split);
+  }
+  int n_tiles = 0;
+#pragma unroll
+  for (int s = 0; s < NQ; ++s) {
+    cnt[s] = max(0, min(cnt[s], hi) - lo);
+    n_tiles = max(n_tiles, cnt[s]);
+  }
+
   // Masked calls: the tiles that hold a valid key, in order, with the top bit
   // set when some of their keys are masked; all other tiles are skipped.  (Key
   // ranges beyond the list's room look every tile's mask up instead.)
@@ -479,7 +496,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     const int s = warp >> 2;             // query tile of this warpgroup
     const int row = threadIdx.x & 127;   // its row, the TMEM lane
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
-    const int tok = row / L.Gc, g = w.g0 + row - tok * L.Gc;
+    const int tok = divide(row, L.Gc, L.gc_inv), g = w.g0 + row - tok * L.Gc;
     const int t0 = w.tok0 + s * L.T;
     const bool real = tok < L.T && t0 + tok < w.n_new && g < L.G;
     // keys this row sees; keys every row of the tile sees
@@ -585,8 +602,11 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     __syncwarp();
     tc_fence_after();
     if (ok && L.split == 1) {
+      // Rows through shared memory, over the query tile whose products are done
+      // (its layout), then out by TMA; a tile cut short by the sequence's end (or
+      // the group's) in runs of whole rows by its threads.
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      bf16* dst = a.out + (int64_t)(w.q_row0 + t0 + tok) * a.out_stride + (int64_t)(w.kvh * L.G + g) * DH;
+      uint8_t* tile = smem + s * C::QBYTES;
 #pragma unroll 1
       for (int d = 0; d < DH; d += 32) {
         uint32_t o[32];
@@ -595,16 +615,38 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
           tmem_ld_wait();
           landed(o);
         }
-        if (real) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t v[4];
+        for (int q = 0; q < 4; ++q) {
+          uint32_t v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = l > 0.f ? bf16x2(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv)
-                             : 0u;
-            *reinterpret_cast<uint4*>(dst + d + 8 * q) = make_uint4(v[0], v[1], v[2], v[3]);
-          }
+          for (int e = 0; e < 4; ++e)
+            v[e] = l > 0.f ? bf16x2(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv)
+                           : 0u;
+          *reinterpret_cast<uint4*>(tile + (d >> 6) * (128 * 128) + sw128_offset(row, ((d & 32) >> 3) + q)) =
+              make_uint4(v[0], v[1], v[2], v[3]);
+        }
+      }
+      if (t0 + L.T <= w.n_new && w.g0 + L.Gc <= L.G) {
+        fence_proxy_async_smem();
+        asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory");
+        if (row == 0) {
+#pragma unroll
+          for (int d = 0; d < DB; ++d)
+            tma_store_3d(&omap, tile + d * (128 * 128), d * 64, w.kvh * L.G + w.g0, w.q_row0 + t0);
+          bulk_commit();
+          bulk_wait_read_all();
+        }
+      } else {
+        __syncwarp();  // a warp stores the 32 rows it wrote
+        constexpr int CPR = DH / 8, RPI = 32 / CPR;  // pieces of a row; rows an instruction
+        const int r0 = 32 * (warp & 3) + lane / CPR, ch = lane % CPR;
+        bf16* out0 = a.out + (int64_t)(w.q_row0 + t0) * a.out_stride + (int64_t)(w.kvh * L.G + w.g0) * DH + 8 * ch;
+#pragma unroll 4
+        for (int r = r0; r < 32 * (warp & 3) + 32; r += RPI) {
+          const int rt = divide(r, L.Gc, L.gc_inv), rg = r - rt * L.Gc;
+          if (rt < L.T && t0 + rt < w.n_new && w.g0 + rg < L.G)
+            *reinterpret_cast<uint4*>(out0 + rt * a.out_stride + rg * DH) =
+                *reinterpret_cast<const uint4*>(tile + (ch >> 3) * (128 * 128) + sw128_offset(r, ch & 7));
         }
       }
     } else if (L.split > 1) {
@@ -646,9 +688,9 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     const Unit w = find_unit<DH>(a, L, bx / L.split);
     const int rank = (int)cluster_rank();
     // rank r merges its share of the rows: the weight 2^(m_p - m) / l of every
-    // split first, then DH / 4 four-dim pieces a row, four pieces a thread at once
+    // split first, then DH / 4 four-dim pieces a row
     const int share = NQ * 128 / L.split;
-    constexpr int PER = DH / 4, UN = 4;
+    constexpr int PER = DH / 4, UN = 2;
     const uint32_t base = smem_u32(smem), ml = smem_u32(smem + C::ML);
     float* wt = reinterpret_cast<float*>(smem + C::WT);  // [share][split]
     for (int i = threadIdx.x; i < share; i += C::THREADS) {
@@ -670,32 +712,38 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
         if (p < L.split) wt[i * L.split + p] = l > 0.f ? x[p].x / l : 0.f;
     }
     __syncthreads();
+    uint32_t peer[8];
+#pragma unroll
+    for (int p = 0; p < 8; ++p) peer[p] = mapa(base, p < L.split ? p : 0);
     for (int i0 = threadIdx.x; i0 < share * PER; i0 += UN * C::THREADS) {
-      float4 o[UN];
+      float4 v[UN][8];  // every split's piece in flight at once
 #pragma unroll
-      for (int e = 0; e < UN; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int p = 0; p < L.split; ++p) {
-        const uint32_t peer = mapa(base, p);
+      for (int e = 0; e < UN; ++e) {
+        const int i = min(i0 + e * C::THREADS, share * PER - 1), r = rank * share + i / PER, q = i % PER;
 #pragma unroll
-        for (int e = 0; e < UN; ++e) {
-          const int i = min(i0 + e * C::THREADS, share * PER - 1), r = rank * share + i / PER, q = i % PER;
-          const float4 v = ld_cluster_f4(peer + r * (DH * 4) + ((q ^ (r & 7)) << 4));
-          const float f = wt[(i / PER) * L.split + p];
-          o[e].x += f * v.x;
-          o[e].y += f * v.y;
-          o[e].z += f * v.z;
-          o[e].w += f * v.w;
-        }
+        for (int p = 0; p < 8; ++p)
+          v[e][p] = p < L.split ? ld_cluster_f4(peer[p] + r * (DH * 4) + ((q ^ (r & 7)) << 4))
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
       }
 #pragma unroll
       for (int e = 0; e < UN; ++e) {
         const int i = i0 + e * C::THREADS, r = rank * share + i / PER, q = i % PER;
         const int s = r >> 7, rr = r & 127;
-        const int tok = rr / L.Gc, g = w.g0 + rr - tok * L.Gc;
+        const int tok = divide(rr, L.Gc, L.gc_inv), g = w.g0 + rr - tok * L.Gc;
         const int t = w.tok0 + s * L.T + tok;
         if (i >= share * PER || tok >= L.T || t >= w.n_new || g >= L.G) continue;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int p = 0; p < 8; ++p)
+          if (p < L.split) {
+            const float f = wt[(i / PER) * L.split + p];
+            o.x += f * v[e][p].x;
+            o.y += f * v[e][p].y;
+            o.z += f * v[e][p].z;
+            o.w += f * v[e][p].w;
+          }
         *reinterpret_cast<uint2*>(a.out + (int64_t)(w.q_row0 + t) * a.out_stride + (int64_t)(w.kvh * L.G + g) * DH +
-                                  4 * q) = make_uint2(bf16x2(o[e].x, o[e].y), bf16x2(o[e].z, o[e].w));
+                                  4 * q) = make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
       }
     }
     __syncthreads();
@@ -712,6 +760,8 @@ cudaError_t launch(const PromptAttnArgs& a, int sm_count, cudaStream_t st) {
   L.hc = (L.G + 127) / 128;
   L.Gc = (L.G + L.hc - 1) / L.hc;
   L.T = 128 / L.Gc;
+  L.per = a.Hkv * L.hc;
+  L.gc_inv = L.Gc > 1 ? (uint32_t)(((1ull << 32) + L.Gc - 1) / L.Gc) : 0;
   // sequences with queries, longest key ranges first
   int n = 0;
   for (int b = 0; b < a.batch; ++b)
@@ -729,14 +779,21 @@ cudaError_t launch(const PromptAttnArgs& a, int sm_count, cudaStream_t st) {
     if (units > 0x7fffffff / 8) return cudaErrorInvalidConfiguration;
   }
   L.work_cu[n] = (int)units;
-  // few units over long key ranges: split the keys over a cluster while every
-  // cluster stays resident and a split keeps four tiles of the longest range
+  L.per_inv = L.per > 1 && units * L.per < ((int64_t)1 << 32) ? (uint32_t)(((1ull << 32) + L.per - 1) / L.per) : 0;
+  // Few units over long key ranges: split the keys over the CTAs of a cluster,
+  // as many as stay resident together, while a CTA keeps two tiles.  The merge
+  // costs about as much as five tiles, so halves pay for longer ranges only:
+  // 16 rows over 1016 keys 32/8/128 12.0 us split by 4, 14.6 unsplit; 400 tokens
+  // 13.7 us split by 2, 10.9 unsplit.
   const int tiles = (a.kv_len[L.order[0]] + C::BK - 1) / C::BK;
   L.split = 1;
-  while (L.split < 8 && units * L.split * 2 <= sm_count && tiles >= L.split * 8) L.split *= 2;
+  while (L.split < 8 && units * L.split * 2 <= sm_count) L.split *= 2;
+  while (L.split > 1 && tiles < (L.split >= 4 ? 2 * L.split : (C::BK == 64 ? 12 : 8))) L.split /= 2;
 
-  CUtensorMap qmap, kmap, vmap;
+  CUtensorMap qmap, kmap, vmap, omap;
   cudaError_t e = make_bf16_3d_map(&qmap, a.q, {DH, a.Hq, a.cu_q[a.batch]}, {DH, (long)a.q_stride}, {64, L.Gc, L.T});
+  if (e == cudaSuccess)
+    e = make_bf16_3d_map(&omap, a.out, {DH, a.Hq, a.cu_q[a.batch]}, {DH, (long)a.out_stride}, {64, L.Gc, L.T});
   if (e == cudaSuccess)
     e = make_bf16_3d_map(&kmap, a.k, {64, (long)a.cache_rows, (long)a.Hkv * C::DB}, {(long)a.kv_stride, 64},
                          {64, C::BK, C::DB});
@@ -755,8 +812,8 @@ cudaError_t launch(const PromptAttnArgs& a, int sm_count, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = L.split > 1 ? 1 : 0;
-  return a.key_mask ? cudaLaunchKernelEx(&cfg, k_prompt_attn<DH, true>, qmap, kmap, vmap, a, L)
-                    : cudaLaunchKernelEx(&cfg, k_prompt_attn<DH, false>, qmap, kmap, vmap, a, L);
+  return a.key_mask ? cudaLaunchKernelEx(&cfg, k_prompt_attn<DH, true>, qmap, kmap, vmap, omap, a, L)
+                    : cudaLaunchKernelEx(&cfg, k_prompt_attn<DH, false>, qmap, kmap, vmap, omap, a, L);
 }
 
 }  // namespace
