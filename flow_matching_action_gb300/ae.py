@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Dict, Optional, Sequence
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -242,41 +243,33 @@ def ae_prefill_prompts(ctx, args: ae_prefill_prompts_args) -> None:
     _check(lib().ae_prefill_prompts(ctx, ctypes.byref(args)), ctx)
 
 
-_dtypes = None
+_BF16 = _I32 = _I64 = _U8 = None  # torch dtypes: this module imports torch only once tensors are passed
 
 
-def _torch_dtypes():
-    """(bf16, int32, int64, uint8): the module works without torch until tensors are passed."""
-    global _dtypes
-    if _dtypes is None:
-        import torch
-        _dtypes = (torch.bfloat16, torch.int32, torch.int64, torch.uint8)
-    return _dtypes
+def _load_dtypes():
+    global _BF16, _I32, _I64, _U8
+    import torch
+    _BF16, _I32, _I64, _U8 = torch.bfloat16, torch.int32, torch.int64, torch.uint8
 
 
-_BF16, _I32, _I64, _U8 = range(4)
-
-
-def _rows(name: str, t, width: int, rows: Optional[int] = None):
+def _rows(name: str, t, width: int, rows: int = -1):
     """(pointer, row stride) of a bf16 CUDA tensor [rows, width] whose rows are contiguous."""
-    shape, dt = t.shape, _dtypes or _torch_dtypes()
-    if len(shape) != 2 or shape[1] != width or (rows is not None and shape[0] != rows):
-        raise ValueError(f"{name}: shape {tuple(shape)}, expected [{'rows' if rows is None else rows}, {width}]")
-    if t.dtype is not dt[_BF16] or not t.is_cuda:
+    shape, step = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != width or (rows >= 0 and shape[0] != rows):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [{'rows' if rows < 0 else rows}, {width}]")
+    if t.dtype is not _BF16 or not t.is_cuda:
         raise ValueError(f"{name}: expected a bf16 CUDA tensor, got {t.dtype} on {t.device}")
-    step = t.stride()
     if step[1] != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
     return t.data_ptr(), step[0] if shape[0] > 1 else width  # one row has no stride
 
 
-def _vec(name: str, t, dtype: int, n: int):
-    """Pointer of a contiguous CUDA tensor of n elements, or None."""
+def _vec(name: str, t, dtype, n: int) -> int:
+    """Pointer of a contiguous CUDA tensor of n elements, 0 for None."""
     if t is None:
-        return None
-    want = (_dtypes or _torch_dtypes())[dtype]
-    if t.dtype is not want or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
-        raise ValueError(f"{name}: expected {n} contiguous {want} elements on the GPU, got {tuple(t.shape)} "
+        return 0
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name}: expected {n} contiguous {dtype} elements on the GPU, got {tuple(t.shape)} "
                          f"{t.dtype} on {t.device}")
     return t.data_ptr()
 
@@ -288,8 +281,26 @@ def _host_array(ctype, x):
     return (ctype * len(x))(*x)
 
 
-def _addr(arr):
-    return None if arr is None else ctypes.addressof(arr)
+def _addr(arr) -> int:
+    return 0 if arr is None else ctypes.addressof(arr)
+
+
+# The argument structs of the operators as packed bytes, in C's own layout ("@"):
+# a third of the time of filling a ctypes structure, which shows in a call that
+# takes the GPU a few microseconds.
+_ROPE_ARGS = struct.Struct("@iiPqPPfPPPPqPqPPq")
+_PROMPT_ARGS = struct.Struct("@iiPPPqPqPPqPfPq")
+_TOKEN_ARGS = struct.Struct("@iiPPqPqPPqPfPq")
+_packed = {}
+
+
+def _call_packed(name: str, ctx, args: bytes) -> None:
+    fn = _packed.get(name)
+    if fn is None:
+        fn = _packed[name] = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_char_p)((name, lib()))
+    status = fn(ctx, args)
+    if status != AE_OK:
+        raise AEError(status, _msg(ctx))
 
 
 def _pairs(pair_axis, pair_freq, half: int):
@@ -361,6 +372,7 @@ class ActionExpert:
         self.dims = dims
         self.config = make_config(dims, dtype, fp8_weights)
         self._wstruct = make_weights(weights)
+        _load_dtypes()
         self._q_dim, self._kv_dim = dims.n_q_heads * dims.head_dim, dims.n_kv_heads * dims.head_dim
         self.ctx = ae_create(self.config, self._wstruct, max_batch, max_prefix_rows, stream)
         self._bound = None
@@ -398,10 +410,10 @@ class ActionExpert:
         v, v_stride = _rows("v_cache", v_cache, kvd, cache_rows)
         if v_stride != k_stride:
             raise ValueError("k_cache and v_cache have different row strides")
-        ae_qk_norm_rope(self.ctx, ae_qk_norm_rope_args(
+        axis = None if pair_axis is None else (ctypes.c_uint8 * (dh // 2)).from_buffer_copy(pair_axis)
+        _call_packed("ae_qk_norm_rope", self.ctx, _ROPE_ARGS.pack(
             n, axes, x, x_stride, _vec("q_norm", q_norm, _BF16, dh), _vec("k_norm", k_norm, _BF16, dh), norm_offset,
-            _vec("positions", positions, _I32, axes * n), pair_axis, _addr(freq), _vec("kv_rows", kv_rows, _I64, n),
-            cache_rows, q, q_stride, k, v, k_stride))
+            _vec("positions", positions, _I32, axes * n), _addr(axis), _addr(freq), _vec("kv_rows", kv_rows, _I64, n), cache_rows, q, q_stride, k, v, k_stride))
 
     def prompt_attention(self, q, k, v, cu_q, kv_row0=None, kv_len=None, key_mask=None, causal: bool = True,
                          scale: float = 0.0, out=None):
@@ -427,7 +439,7 @@ class ActionExpert:
         if v_stride != k_stride:
             raise ValueError("k and v have different row strides")
         op, o_stride = _rows("out", out, self._q_dim, rows)
-        ae_prompt_attention(self.ctx, ae_prompt_attention_args(
+        _call_packed("ae_prompt_attention", self.ctx, _PROMPT_ARGS.pack(
             batch, 1 if causal else 0, _addr(cu), _addr(row0), _addr(lens), cache_rows, qp, q_stride, kp, vp, k_stride,
             _vec("key_mask", key_mask, _U8, cache_rows), scale, op, o_stride))
         return out
@@ -447,7 +459,7 @@ class ActionExpert:
         if v_stride != k_stride:
             raise ValueError("k and v have different row strides")
         op, o_stride = _rows("out", out, self._q_dim, n)
-        ae_token_attention(self.ctx, ae_token_attention_args(
+        _call_packed("ae_token_attention", self.ctx, _TOKEN_ARGS.pack(
             n, max_len, _vec("kv_row0", kv_row0, _I64, n), _vec("kv_len", kv_len, _I32, n), cache_rows, qp, q_stride,
             kp, vp, k_stride, _vec("key_mask", key_mask, _U8, cache_rows), scale, op, o_stride))
         return out

@@ -607,44 +607,48 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
       // the group's) in runs of whole rows by its threads.
       const float inv = l > 0.f ? 1.f / l : 0.f;
       uint8_t* tile = smem + s * C::QBYTES;
+      const bool whole = t0 + L.T <= w.n_new && w.g0 + L.Gc <= L.G;
 #pragma unroll 1
-      for (int d = 0; d < DH; d += 32) {
-        uint32_t o[32];
+      for (int d = 0; d < DB; ++d) {
+        uint32_t o[2][32];
         if (n > 0) {
-          tmem_ld32_start(tm_o + d, o);
+          tmem_ld32_start(tm_o + 64 * d, o[0]);
+          tmem_ld32_start(tm_o + 64 * d + 32, o[1]);
           tmem_ld_wait();
-          landed(o);
+          landed(o[0]);
+          landed(o[1]);
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 8; ++q) {
           uint32_t v[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            v[e] = l > 0.f ? bf16x2(__uint_as_float(o[8 * q + 2 * e]) * inv, __uint_as_float(o[8 * q + 2 * e + 1]) * inv)
-                           : 0u;
-          *reinterpret_cast<uint4*>(tile + (d >> 6) * (128 * 128) + sw128_offset(row, ((d & 32) >> 3) + q)) =
-              make_uint4(v[0], v[1], v[2], v[3]);
+          for (int e = 0; e < 4; ++e) {
+            const int k = (8 * q + 2 * e) & 31;
+            v[e] = l > 0.f ? bf16x2(__uint_as_float(o[q >> 2][k]) * inv, __uint_as_float(o[q >> 2][k + 1]) * inv) : 0u;
+          }
+          *reinterpret_cast<uint4*>(tile + d * (128 * 128) + sw128_offset(row, q)) = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+        if (whole) {  // a block of 64 dims leaves while the next is staged
+          fence_proxy_async_smem();
+          asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory");
+          if (row == 0) {
+            tma_store_3d(&omap, tile + d * (128 * 128), d * 64, w.kvh * L.G + w.g0, w.q_row0 + t0);
+            bulk_commit();
+          }
         }
       }
-      if (t0 + L.T <= w.n_new && w.g0 + L.Gc <= L.G) {
-        fence_proxy_async_smem();
-        asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory");
-        if (row == 0) {
-#pragma unroll
-          for (int d = 0; d < DB; ++d)
-            tma_store_3d(&omap, tile + d * (128 * 128), d * 64, w.kvh * L.G + w.g0, w.q_row0 + t0);
-          bulk_commit();
-          bulk_wait_read_all();
-        }
+      if (whole) {
+        if (row == 0) bulk_wait_read_all();
       } else {
         __syncwarp();  // a warp stores the 32 rows it wrote
         constexpr int CPR = DH / 8, RPI = 32 / CPR;  // pieces of a row; rows an instruction
         const int r0 = 32 * (warp & 3) + lane / CPR, ch = lane % CPR;
         bf16* out0 = a.out + (int64_t)(w.q_row0 + t0) * a.out_stride + (int64_t)(w.kvh * L.G + w.g0) * DH + 8 * ch;
-#pragma unroll 4
-        for (int r = r0; r < 32 * (warp & 3) + 32; r += RPI) {
+        const int rows = min(32 * (warp & 3) + 32, min(L.T, w.n_new - t0) * L.Gc);
+#pragma unroll 8
+        for (int r = r0; r < rows; r += RPI) {
           const int rt = divide(r, L.Gc, L.gc_inv), rg = r - rt * L.Gc;
-          if (rt < L.T && t0 + rt < w.n_new && w.g0 + rg < L.G)
+          if (w.g0 + rg < L.G)
             *reinterpret_cast<uint4*>(out0 + rt * a.out_stride + rg * DH) =
                 *reinterpret_cast<const uint4*>(tile + (ch >> 3) * (128 * 128) + sw128_offset(r, ch & 7));
         }

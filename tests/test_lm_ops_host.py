@@ -163,3 +163,20 @@ def test_nothing_to_do_is_ok(make_context):
     ae.ae_prompt_attention(c, prompt_args(cu=(0, 0, 0), row0=(0, 5), lens=(0, 3), q=None, k=None, v=None, out=None))
     ae.ae_prefill_prompts(c, prefill_args(cu=(0, 0), embeddings=None, out_k=None, out_v=None, positions=None))
     ae.ae_token_attention(c, token_args(batch=0, q=None, k=None, v=None, out=None))
+
+
+@pytest.mark.parametrize("packed,fields", [(ae._ROPE_ARGS, ae.ae_qk_norm_rope_args),
+                                           (ae._PROMPT_ARGS, ae.ae_prompt_attention_args),
+                                           (ae._TOKEN_ARGS, ae.ae_token_attention_args)])
+def test_packed_arguments_have_the_structs_layout(packed, fields):
+    """Distinct values packed into bytes read back, field by field, through the ctypes structure."""
+    values = list(range(1, len(fields._fields_) + 1))
+    s = fields.from_buffer_copy(packed.pack(*values).ljust(ctypes.sizeof(fields), b"\0"))
+    assert packed.size <= ctypes.sizeof(fields)
+    for (name, kind), v in zip(fields._fields_, values):
+        offset = getattr(fields, name).offset
+        if kind is ctypes.c_char_p:  # a pointer this test must not follow
+            got = ctypes.c_size_t.from_buffer_copy(bytes(s)[offset:offset + 8]).value
+        else:
+            got = getattr(s, name)
+        assert got == v, name
