@@ -40,9 +40,13 @@ constexpr float kRaise = 8.f;  // log2: raise the exponent reference past this
 template <int DH>
 struct Cfg {
   static constexpr int NQ = DH == 256 ? 1 : 2;
-  static constexpr int BK = DH == 256 ? 64 : 128;
+  static constexpr int BK = 128;                   // keys of a tile
   static constexpr int DB = DH / 64;               // 64-dim blocks of a row
-  static constexpr int SLOT = BK * DH * 2;         // bytes of a K or V tile
+  // a ring slot holds a K or V tile; at head_dim 256 half of one: all keys of half
+  // the dims of K, all dims of half the keys of V
+  static constexpr int PARTS = DH == 256 ? 2 : 1;
+  static constexpr int DBK = DB / PARTS, BKV = BK / PARTS;
+  static constexpr int SLOT = BK * DH * 2 / PARTS;
   static constexpr int NS = DH == 64 ? 8 : 5;      // ring slots
   static constexpr int QBYTES = 128 * DH * 2;      // bytes of a query tile
   static constexpr int THREADS = NQ * 128 + 128;   // + a warpgroup of which two warps work
@@ -334,13 +338,14 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
   // K0 K1 V0 K2 V1 .. (NQ = 1).
   int loaded = 0;
   auto load = [&]() {
-    const int i = loaded;
+    const int i = loaded / C::PARTS, h = loaded % C::PARTS;
     const bool is_v = NQ == 2 ? (i & 1) : (i > 0 && ((i & 1) == 0 || i + 1 == 2 * n_tiles));
     const int t = NQ == 2 ? i >> 1 : (is_v ? (i + 1 == 2 * n_tiles ? n_tiles - 1 : (i >> 1) - 1) : (i + 1) >> 1);
-    const int slot = i % NS;
+    const int slot = loaded % NS;
     mbar_arrive_expect_tx(&B->full[slot], C::SLOT);
     tma_load_3d_nohint(smem + C::RING + slot * C::SLOT, is_v ? &vmap : &kmap, &B->full[slot], 0,
-                       (int)(w.kv_row0 + (int64_t)(lo + tile_at(t)) * BK), w.kvh * DB);
+                       (int)(w.kv_row0 + (int64_t)(lo + tile_at(t)) * BK) + (is_v ? h * C::BKV : 0),
+                       w.kvh * DB + (is_v ? 0 : h * C::DBK));
     ++loaded;
   };
   if (warp == C::W_LOAD && lane == 0 && n_tiles > 0) {
@@ -351,7 +356,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
       for (int d = 0; d < DB; ++d)
         tma_load_3d_nohint(smem + s * C::QBYTES + d * (128 * 128), &qmap, &B->q, d * 64, w.kvh * L.G + w.g0,
                            w.q_row0 + w.tok0 + s * L.T);
-    while (loaded < NS && loaded < 2 * n_tiles) load();
+    while (loaded < NS && loaded < 2 * C::PARTS * n_tiles) load();
   }
   tc_fence_before();
   __syncthreads();
@@ -363,7 +368,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
   if (warp == C::W_LOAD) {
     // ---------------------------------------------------------------- loads
     if (lane == 0 && n_tiles > 0) {
-      while (loaded < 2 * n_tiles &&
+      while (loaded < 2 * C::PARTS * n_tiles &&
              mbar_wait(&B->empty[loaded % NS], (uint32_t)((loaded / NS) & 1) ^ 1u, abort_flag, a.status))
         load();
       // every copy lands before the CTA's shared memory is released, also after a failure
@@ -378,29 +383,30 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     bool ok = n_tiles == 0 || warp_wait(&B->q, 0, abort_flag, a.status);
     auto wait_slot = [&](int i) { return warp_wait(&B->full[i % NS], (uint32_t)(i / NS) & 1u, abort_flag, a.status); };
     const uint64_t q_desc = sdesc_sw128(smem_u32(smem)), k_desc = sdesc_sw128(smem_u32(smem) + C::RING),
-                   v_desc = sdesc_sw128_mn(smem_u32(smem) + C::RING, BK * 128, 1024);
-    auto qk = [&](int s, int buf, int slot) {
+                   v_desc = sdesc_sw128_mn(smem_u32(smem) + C::RING, C::BKV * 128, 1024);
+    // part h of S = Q K^T (of the dims) and of O += P V (of the keys)
+    auto qk = [&](int s, int buf, int slot, int h) {
       const uint64_t ad = q_desc + (uint64_t)(s * C::QBYTES >> 4), bd = k_desc + (uint64_t)(slot * C::SLOT >> 4);
       if (elect_one()) {
 #pragma unroll
-        for (int d = 0; d < DB; ++d)
+        for (int d = 0; d < C::DBK; ++d)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_bf16(tmem + (uint32_t)(buf * BK), ad + d * (128 * 128 >> 4) + 2 * k, bd + d * (BK * 128 >> 4) + 2 * k,
-                     idesc_s, (d > 0 || k > 0) ? 1u : 0u);
-        mma_commit(&B->s[buf]);
+            mma_bf16(tmem + (uint32_t)(buf * BK), ad + (h * C::DBK + d) * (128 * 128 >> 4) + 2 * k,
+                     bd + d * (BK * 128 >> 4) + 2 * k, idesc_s, (h > 0 || d > 0 || k > 0) ? 1u : 0u);
+        if (h == C::PARTS - 1) mma_commit(&B->s[buf]);
       }
       __syncwarp();
     };
-    auto pv = [&](int s, int buf, int slot, bool first, uint64_t* done) {
+    auto pv = [&](int s, int buf, int slot, bool first, uint64_t* done, int h) {
       const uint64_t bd = v_desc + (uint64_t)(slot * C::SLOT >> 4);
       const uint32_t acc = first ? 0u : 1u;
       if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < BK / 16; ++k)
-          mma_bf16_ts(tmem + (uint32_t)(C::O0 + s * DH), tmem + (uint32_t)(buf * BK + 8 * k), bd + k * (2048 >> 4),
-                      idesc_o, k > 0 ? 1u : acc);
-        if (done != nullptr) mma_commit(done);
+        for (int k = 0; k < C::BKV / 16; ++k)
+          mma_bf16_ts(tmem + (uint32_t)(C::O0 + s * DH), tmem + (uint32_t)(buf * BK + 8 * (h * (C::BKV / 16) + k)),
+                      bd + k * (2048 >> 4), idesc_o, (h > 0 || k > 0) ? 1u : acc);
+        if (done != nullptr && h == C::PARTS - 1) mma_commit(done);
       }
       __syncwarp();
     };
@@ -408,20 +414,20 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
       if (elect_one()) mma_commit(&B->empty[slot]);
       __syncwarp();
     };
-    // zero the V rows of tile i that no query may see
-    auto clean_v = [&](int i, int slot) {
-      const int key0 = (lo + tile_at(i)) * BK;
+    // zero the V rows of part h of tile i that no query may see
+    auto clean_v = [&](int i, int slot, int h) {
+      const int key0 = (lo + tile_at(i)) * BK + h * C::BKV;
       const bool holes = holes_at(i);
-      if (!holes && key0 + BK <= w.n_keys) return;
-      uint32_t bits[BK / 32];
-      tile_bits<BK>(holes ? mask : nullptr, key0, w.n_keys, bits);
+      if (!holes && key0 + C::BKV <= w.n_keys) return;
+      uint32_t bits[C::BKV / 32];
+      tile_bits<C::BKV>(holes ? mask : nullptr, key0, w.n_keys, bits);
       uint32_t all = 0xffffffffu;
 #pragma unroll
-      for (int k = 0; k < BK / 32; ++k) all &= bits[k];
+      for (int k = 0; k < C::BKV / 32; ++k) all &= bits[k];
       if (all == 0xffffffffu) return;
       uint8_t* v = smem + C::RING + slot * C::SLOT;
 #pragma unroll
-      for (int k = 0; k < BK / 32; ++k)
+      for (int k = 0; k < C::BKV / 32; ++k)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           // 16-byte piece lane + 32 e of this word's 32 rows: row (lane + 32 e) / 8
@@ -429,7 +435,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
           if (!((bits[k] >> r) & 1u))
 #pragma unroll
             for (int d = 0; d < DB; ++d)
-              *reinterpret_cast<uint4*>(v + d * (BK * 128) + (32 * k + r) * 128 + (lane & 7) * 16) =
+              *reinterpret_cast<uint4*>(v + d * (C::BKV * 128) + (32 * k + r) * 128 + (lane & 7) * 16) =
                   make_uint4(0u, 0u, 0u, 0u);
         }
       fence_proxy_async_smem();
@@ -439,22 +445,22 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
       if (n_tiles > 0 && ok && (ok = wait_slot(0))) {
 #pragma unroll
         for (int s = 0; s < NQ; ++s)
-          if (cnt[s] > 0) qk(s, s, 0);
+          if (cnt[s] > 0) qk(s, s, 0, 0);
         release(0);
         c = 1;
       }
       for (int i = 0; i < n_tiles && ok; ++i) {
         // slot c: V of tile i, slot c + 1: K of tile i + 1
         if (!(ok = wait_slot(c))) break;
-        clean_v(i, c % NS);
+        clean_v(i, c % NS, 0);
         if (i + 1 < n_tiles && !(ok = wait_slot(c + 1))) break;
 #pragma unroll
         for (int s = 0; s < NQ; ++s) {
           if (ok && i < cnt[s]) {
             if (!(ok = warp_wait(&B->p[s], (uint32_t)i & 1u, abort_flag, a.status))) break;
             tc_fence_after();
-            pv(s, s, c % NS, i == 0, i + 1 == cnt[s] ? &B->o[s] : nullptr);
-            if (i + 1 < cnt[s]) qk(s, s, (c + 1) % NS);
+            pv(s, s, c % NS, i == 0, i + 1 == cnt[s] ? &B->o[s] : nullptr, 0);
+            if (i + 1 < cnt[s]) qk(s, s, (c + 1) % NS, 0);
           }
         }
         if (!ok) break;
@@ -463,25 +469,33 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
         c += 2;
       }
     } else {
-      if (n_tiles > 0 && ok && (ok = wait_slot(0))) {
-        qk(0, 0, 0);
-        release(0);
-        c = 1;
-      }
-      for (int i = 0; i < n_tiles && ok; ++i) {
-        if (i + 1 < n_tiles) {
-          if (!(ok = wait_slot(c))) break;
-          qk(0, (i + 1) & 1, c % NS);
+#pragma unroll
+      for (int h = 0; h < C::PARTS; ++h)
+        if (n_tiles > 0 && ok && (ok = wait_slot(c))) {
+          qk(0, 0, c % NS, h);
           release(c % NS);
           ++c;
         }
-        if (!(ok = wait_slot(c))) break;
-        clean_v(i, c % NS);
-        if (!(ok = warp_wait(&B->p[i & 1], (uint32_t)(i >> 1) & 1u, abort_flag, a.status))) break;
-        tc_fence_after();
-        pv(0, i & 1, c % NS, i == 0, &B->o[i & 1]);
-        release(c % NS);
-        ++c;
+      for (int i = 0; i < n_tiles && ok; ++i) {
+#pragma unroll
+        for (int h = 0; h < C::PARTS; ++h)
+          if (ok && i + 1 < n_tiles && (ok = wait_slot(c))) {
+            qk(0, (i + 1) & 1, c % NS, h);
+            release(c % NS);
+            ++c;
+          }
+#pragma unroll
+        for (int h = 0; h < C::PARTS; ++h) {
+          if (!ok || !(ok = wait_slot(c))) break;
+          clean_v(i, c % NS, h);
+          if (h == 0) {
+            if (!(ok = warp_wait(&B->p[i & 1], (uint32_t)(i >> 1) & 1u, abort_flag, a.status))) break;
+            tc_fence_after();
+          }
+          pv(0, i & 1, c % NS, i == 0, &B->o[i & 1], h);
+          release(c % NS);
+          ++c;
+        }
       }
     }
     if (!ok && lane == 0) {  // MMAs in flight must finish before tensor memory is freed
@@ -792,7 +806,7 @@ cudaError_t launch(const PromptAttnArgs& a, int sm_count, cudaStream_t st) {
   const int tiles = (a.kv_len[L.order[0]] + C::BK - 1) / C::BK;
   L.split = 1;
   while (L.split < 8 && units * L.split * 2 <= sm_count) L.split *= 2;
-  while (L.split > 1 && tiles < (L.split >= 4 ? 2 * L.split : (C::BK == 64 ? 12 : 8))) L.split /= 2;
+  while (L.split > 1 && tiles < (L.split >= 4 ? 2 * L.split : 8)) L.split /= 2;
 
   CUtensorMap qmap, kmap, vmap, omap;
   cudaError_t e = make_bf16_3d_map(&qmap, a.q, {DH, a.Hq, a.cu_q[a.batch]}, {DH, (long)a.q_stride}, {64, L.Gc, L.T});
@@ -800,10 +814,10 @@ cudaError_t launch(const PromptAttnArgs& a, int sm_count, cudaStream_t st) {
     e = make_bf16_3d_map(&omap, a.out, {DH, a.Hq, a.cu_q[a.batch]}, {DH, (long)a.out_stride}, {64, L.Gc, L.T});
   if (e == cudaSuccess)
     e = make_bf16_3d_map(&kmap, a.k, {64, (long)a.cache_rows, (long)a.Hkv * C::DB}, {(long)a.kv_stride, 64},
-                         {64, C::BK, C::DB});
+                         {64, C::BK, C::DBK});
   if (e == cudaSuccess)
     e = make_bf16_3d_map(&vmap, a.v, {64, (long)a.cache_rows, (long)a.Hkv * C::DB}, {(long)a.kv_stride, 64},
-                         {64, C::BK, C::DB});
+                         {64, C::BKV, C::DB});
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * L.split));
