@@ -275,8 +275,8 @@ def _vec(name: str, t, dtype, n: int) -> int:
 
 
 def _host_array(ctype, x):
-    """A host array of a sequence (kept as it is when it already is a ctypes array), or None."""
-    if x is None or isinstance(x, ctypes.Array):
+    """A host array of a sequence (kept as it is when it already is one of that type), or None."""
+    if x is None or (isinstance(x, ctypes.Array) and x._type_ is ctype):
         return x
     return (ctype * len(x))(*x)
 

@@ -103,8 +103,8 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
 #pragma unroll
   for (int i = 0; i < PAIRS; ++i) {
     turn[i] = a.turn_table ? a.turn_table[lane + 32 * i] : a.turn[lane + 32 * i];
-    axis[i] = a.n_axes > 1 ? a.axis[lane + 32 * i] * a.tokens : 0;
-    pos[i] = item < items ? a.positions[(int64_t)axis[i] + t] : 0;
+    axis[i] = a.n_axes > 1 ? a.axis[lane + 32 * i] : 0;
+    pos[i] = item < items ? a.positions[(int64_t)axis[i] * a.tokens + t] : 0;
   }
   if (item < items) row = a.kv_rows ? a.kv_rows[t] : t;
   if (a.q_norm != nullptr || a.k_norm != nullptr)
@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks)
     const int t1 = item / parts, h1 = (item - t1 * parts) * HPW;
     if (item < items) {  // the next token's positions and cache row
 #pragma unroll
-      for (int i = 0; i < PAIRS; ++i) pos[i] = a.positions[(int64_t)axis[i] + t1];
+      for (int i = 0; i < PAIRS; ++i) pos[i] = a.positions[(int64_t)axis[i] * a.tokens + t1];
       row = a.kv_rows ? a.kv_rows[t1] : t1;
     }
     bf16* q_row = a.q_out + tok * a.q_stride + 8 * l;

@@ -117,8 +117,10 @@ __global__ void __launch_bounds__(kWarps * 32)
     *abort_flag = 0;
     fence_mbar_init();
     fence_proxy_async_smem();
-    prefetch_tensormap(&kmap);
-    prefetch_tensormap(&vmap);
+    if (a.cache_rows > 0) {  // without rows there are no maps
+      prefetch_tensormap(&kmap);
+      prefetch_tensormap(&vmap);
+    }
   }
 
   // Q as the second operand: heads lane / 4 (+ 8), dims 16 ks + 2 (lane % 4) + {0, 1} (+ 8)

@@ -326,7 +326,8 @@ AE_API ae_status ae_qk_norm_rope(ae_ctx* ctx, const ae_qk_norm_rope_args* args);
  * is left.  Query head h reads KV head h / (n_q_heads / n_kv_heads).  Masked
  * rows may hold anything (NaN included), rows outside the sequences too; the
  * unmasked rows of a sequence must be finite (a non-finite value row may reach
- * every query of its sequence).
+ * every query of its sequence), and so must its scores in fp32.  out may be q
+ * with out_stride == q_stride.
  */
 typedef struct {
   int batch;                 /* sequences, 0..AE_MAX_BATCH                       */
@@ -352,7 +353,7 @@ AE_API ae_status ae_prompt_attention(ae_ctx* ctx, const ae_prompt_attention_args
  * masked ones, all of them (the new token's own K and V are already stored).
  * Lengths and first rows are read on the device, so a captured graph follows
  * them as they grow.  Formula, mask, finiteness and empty rows as in
- * ae_prompt_attention.  A length above max_len, or a range outside the cache,
+ * ae_prompt_attention, and out may be q.  A length above max_len, or a range outside the cache,
  * is cut to what is inside and the context's status becomes AE_ERR_DEVICE.
  */
 typedef struct {

@@ -325,6 +325,34 @@ def test_prompt_attention_most_sequences(experts):
     check_attention(f64(out), ref, mag)
 
 
+@pytest.mark.parametrize("hq,hkv,dh", [(130, 1, 64), (262, 2, 64), (200, 1, 64), (66, 2, 128)])
+def test_prompt_attention_wide_groups(hq, hkv, dh):
+    """Groups of more heads than a query tile has rows, and just above half of them."""
+    ex = _expert(hq, hkv, dh)
+    try:
+        run_prompt(ex, hq, hkv, dh, [1, 5, 40], [0, 130, 3], gap=2)
+        run_token(ex, hq, hkv, dh, [1, 77, 300])
+    finally:
+        ex.close()
+
+
+@pytest.mark.parametrize("hq,hkv,dh", [(8, 1, 256), (12, 4, 64), (32, 8, 128)])
+def test_attention_in_place_of_the_queries(experts, hq, hkv, dh):
+    import torch
+    ex, g = experts(hq, hkv, dh), generator(50)
+    cu, row0, lens = [0, 90, 107], [0, 1300], [1300, 400]
+    q, k, v = normal(g, 107, hq * dh), normal(g, 1700, hkv * dh), normal(g, 1700, hkv * dh)
+    want = ex.prompt_attention(q, k, v, cu, row0, lens)
+    got = q.clone()
+    ex.prompt_attention(got, k, v, cu, row0, lens, out=got)
+    r, n = torch.tensor(row0, device="cuda"), torch.tensor(lens, dtype=torch.int32, device="cuda")
+    token = ex.token_attention(q[:2], k, v, r, n, 1300)
+    over = q[:2].clone()
+    ex.token_attention(over, k, v, r, n, 1300, out=over)
+    ex.synchronize()
+    assert torch.equal(want, got) and torch.equal(token, over)
+
+
 # ---------------------------------------------------------------- token attention
 
 def run_token(ex, hq, hkv, dh, lens, max_len=None, masked=None, seed=0, room=7, scale=0.0):
@@ -370,6 +398,19 @@ def test_token_attention_masks(experts, hq, hkv, dh, masked):
 
 def test_token_attention_many_requests(experts):
     run_token(experts(4, 1, 64), 4, 1, 64, [(37 * i) % 90 for i in range(700)], seed=3)
+
+
+def test_token_attention_without_cache_rows(experts):
+    import torch
+    ex = experts(4, 1, 64)
+    q = torch.ones((3, 256), dtype=torch.bfloat16, device="cuda")
+    k = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    r, n = torch.zeros(3, dtype=torch.int64, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    for max_len in (0, 500):
+        out = torch.full_like(q, 9.0)
+        ex.token_attention(q, k, k, r, n, max_len, out=out)
+        ex.synchronize()
+        assert (out == 0).all()
 
 
 def test_token_attention_scales(experts):

@@ -83,6 +83,22 @@ def test_packed_prompts_match_oracle(causal, norm):
     check(v, rv)
 
 
+@pytest.mark.parametrize("cu", [[0, 1], [0, 0, 1, 2], [0, 7, 7]])
+def test_shortest_prompts(cu):
+    w = synth.make_vlm_weights(TINY, 9)
+    n, half = cu[-1], TINY.head_dim // 2
+    emb = synth.prefix_embeddings(TINY, 9, 1)[:n]
+    pos = np.arange(n)[None]
+    p = Prefill(TINY, w, 1)
+    try:
+        k, v = p(bf16(emb), cu, pos)
+    finally:
+        p.ex.close()
+    rk, rv = lm_ops.prefill_prompts(TINY, w, emb, cu, pos, [0] * half, lm_ops.ladder(TINY.rope_theta, TINY.head_dim))
+    check(k, rk)
+    check(v, rv)
+
+
 def test_equal_bidirectional_prompts_match_the_prefill_oracle():
     """Prompts of one length, bidirectional, one axis, no norms: the values of ae_prefill."""
     w = synth.make_vlm_weights(TINY, 4)
