@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
       for (int d = 0; d < DB; ++d)
         tma_load_3d_nohint(smem + s * C::QBYTES + d * (128 * 128), &qmap, &B->q, d * 64, w.kvh * L.G + w.g0,
                            w.q_row0 + w.tok0 + s * L.T);
-    while (loaded < NS && loaded < 2 * C::PARTS * n_tiles) load();
+    while (loaded < C::PARTS) load();  // the first tile's K; the rest after the CTA has met
   }
   tc_fence_before();
   __syncthreads();
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     // ---------------------------------------------------------------- loads
     if (lane == 0 && n_tiles > 0) {
       while (loaded < 2 * C::PARTS * n_tiles &&
-             mbar_wait(&B->empty[loaded % NS], (uint32_t)((loaded / NS) & 1) ^ 1u, abort_flag, a.status))
+             (loaded < NS || mbar_wait(&B->empty[loaded % NS], (uint32_t)((loaded / NS) & 1) ^ 1u, abort_flag, a.status)))
         load();
       // every copy lands before the CTA's shared memory is released, also after a failure
       mbar_drain(&B->q, 0, a.status);
