@@ -380,7 +380,7 @@ struct PromptAttnArgs {
   int kv_len[AE_MAX_BATCH];
   int64_t kv_row0[AE_MAX_BATCH];
 };
-cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int dh, int sm_count, cudaStream_t s);
+cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int dh, cudaStream_t s);
 cudaError_t prompt_kernel_setup();
 
 struct TokenAttnArgs {

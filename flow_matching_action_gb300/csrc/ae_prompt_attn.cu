@@ -4,20 +4,41 @@
 // T = 128 / G consecutive tokens of a sequence times its G heads (row =
 // token * G + head; T * G <= 128 rows used), so short prompts fill tiles and a
 // causal diagonal covers few keys.  One CTA works on NQ tiles of one
-// (sequence, KV head) and walks the keys in tiles of BK with an online softmax:
-//   S = Q K^T     tcgen05, M = 128, N = BK, fp32 in tensor memory
+// (sequence, KV head) and walks the keys in tiles of 128 with an online softmax:
+//   S = Q K^T       tcgen05, M = N = 128, fp32 in tensor memory
 //   P = 2^(c S - m) one thread per row; bf16 back over the S columns it read
-//   O += P V      tcgen05, P as the TMEM A operand, O stays in tensor memory
+//   O += P V        tcgen05, P as the TMEM A operand, O stays in tensor memory
 // The exponent reference m is raised (and O, l rescaled) only when a row's
 // maximum passes it by more than 2^8, so most tiles skip the rescale and P is
-// at most 2^8; l sums the fp32 weights, P is rounded to bf16 for the tensor
-// cores.
+// at most 2^8; l sums the fp32 weights, P is rounded to bf16 because the tensor
+// cores multiply bf16 (an error of at most 2^-8 of each term, as V's own).
 // Roles: one warpgroup per tile does the softmax, one warp issues TMA loads
 // into a ring of K and V tiles, one warp issues the MMAs.
-//   NQ = 2 (head_dim 64, 128): the two tiles alternate, one tile's MMAs run
-//           under the other's softmax.
-//   NQ = 1 (head_dim 256, whose O fills half of tensor memory): two S buffers,
-//           the next tile's Q K^T runs under this tile's softmax.
+//   head_dim 128: two tiles a CTA alternate, one's MMAs under the other's
+//     softmax; a key tile (two query tiles) takes about 2770 clocks, of which
+//     the MMAs 2048.  32768 tokens 32/8/128: 4.8 ms, 1830 TFLOP/s; bound by the
+//     MMA rate, shared memory's bandwidth near it (operands and TMA writes take
+//     2048 clocks a step too).
+//   head_dim 256: O fills half of tensor memory; one tile, two S buffers, the
+//     next Q K^T under this softmax; K and V in half tiles so that a ring of five
+//     fits beside Q.  8192 tokens 8/1/256: 150 us, 1830 TFLOP/s.  (Key tiles of
+//     64: 191 us, Q K^T of 64 columns is bound by reading Q from shared memory.)
+//   head_dim 64: one tile a CTA and two CTAs a SM, each in the half of tensor
+//     memory, so one's start, end and MMAs run under the other's softmax; bound
+//     by the exponentials and the latency of a softmax step.  8192 tokens
+//     12/4/64: 115 us, 895 TFLOP/s.  (Two tiles sharing K and V in one CTA: 117
+//     us, and 19.8 against 14.6 us for 64 prompts of 100 tokens; four tiles a
+//     CTA on keys of 64: 138 us.)
+// What the MMAs need most is an issue thread that never waits: they are issued
+// under elect.sync on warp-uniform operands (a plain lane test costs 75 clocks
+// per MMA in register moves: 6.7 ms for the 32768 tokens), and both next slots
+// are awaited before the weights.  Tried and slower: two threads a row (430
+// against 351 us, 8192 tokens 32/8/128), P handed over in halves (493 against
+// 461), persistent CTAs that fetch the next unit's tiles under this one's end
+// (356 against 341).
+// A unit's start and end cost about 8500 clocks (first loads and products 5000,
+// output by TMA through the query tile 2400 at 32 bytes a clock); short prompts
+// are bound by them.
 // Keys that a row may not see get score -inf; V rows that no row may see (a
 // sequence's end inside the tile, masked rows) are zeroed in shared memory,
 // since 0 * NaN would reach every row.
@@ -39,7 +60,9 @@ constexpr float kRaise = 8.f;  // log2: raise the exponent reference past this
 
 template <int DH>
 struct Cfg {
-  static constexpr int NQ = DH == 256 ? 1 : 2;
+  static constexpr int NQ = DH == 128 ? 2 : 1;     // query tiles of a CTA
+  static constexpr int SB = DH == 256 ? 2 : 1;     // score buffers of a query tile
+  static constexpr int CTAS = DH == 64 ? 2 : 1;    // resident a SM
   static constexpr int BK = 128;                   // keys of a tile
   static constexpr int DB = DH / 64;               // 64-dim blocks of a row
   // a ring slot holds a K or V tile; at head_dim 256 half of one: all keys of half
@@ -47,11 +70,14 @@ struct Cfg {
   static constexpr int PARTS = DH == 256 ? 2 : 1;
   static constexpr int DBK = DB / PARTS, BKV = BK / PARTS;
   static constexpr int SLOT = BK * DH * 2 / PARTS;
-  static constexpr int NS = DH == 64 ? 8 : 5;      // ring slots
+  static constexpr int NS = 5;                     // ring slots
   static constexpr int QBYTES = 128 * DH * 2;      // bytes of a query tile
-  static constexpr int THREADS = NQ * 128 + 128;   // + a warpgroup of which two warps work
-  // registers: the softmax warpgroups take what the last one gives back
-  static constexpr int REGS_AUX = 104, REGS_MAX = 200;  // 104 + 2 * 200 = 3 * 168, the launch's registers
+  // threads: the softmax warpgroups, then one of which two warps work (loads,
+  // MMAs).  It hands registers to the others where the launch's would not do:
+  // 104 + 2 * 200 = 3 * 168 (NQ = 2), 72 + 184 = 2 * 128 (two CTAs a SM).
+  static constexpr int THREADS = NQ * 128 + 128;
+  static constexpr bool TRADE = NQ == 2 || CTAS == 2;
+  static constexpr int REGS_AUX = NQ == 2 ? 104 : 72, REGS_MAX = NQ == 2 ? 200 : 184;
   static constexpr int W_LOAD = NQ * 4, W_MMA = NQ * 4 + 1;
   // shared memory, from a 1024-byte boundary
   static constexpr int RING = NQ * QBYTES;
@@ -60,10 +86,14 @@ struct Cfg {
   static constexpr int WT = ML + NQ * 128 * 8;     // [rows of this CTA][split] weights of the merge
   static constexpr int LIST = BARS + 256;          // key tiles with valid keys (masked calls): entries, then states
   static constexpr int BYTES = LIST + kListTiles * 3 + 1024;
-  // tensor memory columns
-  static constexpr int O0 = 256;
+  // a split launch asks for more than half an SM's: two CTAs of it would share
+  // SMs while others idle (16 tokens over 4080 keys 4/1/64)
+  static constexpr int SPLIT_BYTES = BYTES > 120 * 1024 ? BYTES : 120 * 1024;
+  // tensor memory columns: scores, then O
+  static constexpr int O0 = NQ * SB * BK, COLS = O0 + NQ * DH <= 256 ? 256 : 512;
   static_assert(WT + NQ * 128 * 4 <= BARS, "fp32 partials fit over the tiles");
-  static_assert(BYTES <= 227 * 1024, "shared memory");
+  static_assert(CTAS * (BYTES + 1024) <= 228 * 1024, "shared memory");
+  static_assert(O0 + NQ * DH <= COLS && CTAS * COLS <= 512, "tensor memory");
 };
 
 struct Launch {
@@ -230,13 +260,13 @@ __device__ __forceinline__ Unit find_unit(const PromptAttnArgs& a, const Launch&
 
 // MASKED: the call has a key mask.
 template <int DH, bool MASKED>
-__global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
     k_prompt_attn(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap,
                   const __grid_constant__ PromptAttnArgs a,
                   const __grid_constant__ Launch L) {
   using C = Cfg<DH>;
-  constexpr int NQ = C::NQ, BK = C::BK, DB = C::DB, NS = C::NS;
+  constexpr int NQ = C::NQ, SB = C::SB, BK = C::BK, DB = C::DB, NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars* B = reinterpret_cast<Bars*>(smem + C::BARS);
@@ -264,7 +294,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     prefetch_tensormap(&omap);
   }
   if (warp == C::W_MMA) {
-    tmem_alloc(&B->tmem, 512);
+    tmem_alloc(&B->tmem, C::COLS);
     tmem_relinquish();
   }
   const Unit w = find_unit<DH>(a, L, blockIdx.x / L.split);
@@ -321,7 +351,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
       }
       if (lane == 0) {
         B->listed[0] = first;
-        B->listed[NQ - 1] = NQ == 1 ? n : (cnt[NQ - 1] >= cnt[0] ? n : 0);
+        if (NQ == 2) B->listed[1] = cnt[NQ - 1] >= cnt[0] ? n : 0;
       }
     }
     __syncthreads();
@@ -339,8 +369,8 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
   int loaded = 0;
   auto load = [&]() {
     const int i = loaded / C::PARTS, h = loaded % C::PARTS;
-    const bool is_v = NQ == 2 ? (i & 1) : (i > 0 && ((i & 1) == 0 || i + 1 == 2 * n_tiles));
-    const int t = NQ == 2 ? i >> 1 : (is_v ? (i + 1 == 2 * n_tiles ? n_tiles - 1 : (i >> 1) - 1) : (i + 1) >> 1);
+    const bool is_v = SB == 1 ? (i & 1) : (i > 0 && ((i & 1) == 0 || i + 1 == 2 * n_tiles));
+    const int t = SB == 1 ? i >> 1 : (is_v ? (i + 1 == 2 * n_tiles ? n_tiles - 1 : (i >> 1) - 1) : (i + 1) >> 1);
     const int slot = loaded % NS;
     mbar_arrive_expect_tx(&B->full[slot], C::SLOT);
     tma_load_3d_nohint(smem + C::RING + slot * C::SLOT, is_v ? &vmap : &kmap, &B->full[slot], 0,
@@ -364,7 +394,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
   const uint32_t tmem = B->tmem;
 
   if (warp >= C::W_LOAD) {
-    if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_AUX));
+    if (C::TRADE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_AUX));
   if (warp == C::W_LOAD) {
     // ---------------------------------------------------------------- loads
     if (lane == 0 && n_tiles > 0) {
@@ -441,7 +471,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
       fence_proxy_async_smem();
       __syncwarp();
     };
-    if (NQ == 2) {
+    if (SB == 1) {
       if (n_tiles > 0 && ok && (ok = wait_slot(0))) {
 #pragma unroll
         for (int s = 0; s < NQ; ++s)
@@ -506,7 +536,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
   }
   } else {
     // ---------------------------------------------------------------- softmax
-    if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_MAX));
+    if (C::TRADE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_MAX));
     const int s = warp >> 2;             // query tile of this warpgroup
     const int row = threadIdx.x & 127;   // its row, the TMEM lane
     const uint32_t lane_off = (uint32_t)(32 * (warp & 3)) << 16;
@@ -523,7 +553,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
     bool ok = true;
     const int n = s == 0 ? cnt[0] : cnt[NQ - 1];
     for (int i = 0; i < n; ++i) {
-      const int buf = NQ == 1 ? i & 1 : s;
+      const int buf = SB == 2 ? i & 1 : s;
       const uint32_t tm_s = tmem + lane_off + (uint32_t)(buf * BK);
       const int key0 = (lo + tile_at(i)) * BK;
       const bool holes = holes_at(i), partial = holes || key0 + BK > open;
@@ -533,7 +563,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
 #pragma unroll
         for (int k = 0; k < BK / 32; ++k) bits[k] &= low_bits(limit - key0, k);
       }
-      if (!warp_wait(&B->s[buf], (uint32_t)(NQ == 1 ? i >> 1 : i) & 1u, abort_flag, a.status)) {
+      if (!warp_wait(&B->s[buf], (uint32_t)(SB == 2 ? i >> 1 : i) & 1u, abort_flag, a.status)) {
         ok = false;
         break;
       }
@@ -567,7 +597,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
       if (i > 0 && __any_sync(0xffffffffu, factor != 1.f)) {
         // O holds tiles 0 .. i-1: with NQ = 2 their P V are done (S of this
         // tile was issued behind them), with NQ = 1 the last one may still run
-        if (NQ == 1 && !warp_wait(&B->o[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, abort_flag, a.status)) {
+        if (SB == 2 && !warp_wait(&B->o[(i - 1) & 1], (uint32_t)((i - 1) >> 1) & 1u, abort_flag, a.status)) {
           ok = false;
           break;
         }
@@ -611,7 +641,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
       if (lane == 0) mbar_arrive(&B->p[buf]);
     }
     if (ok && n > 0)
-      ok = NQ == 1 ? warp_wait(&B->o[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u, abort_flag, a.status)
+      ok = SB == 2 ? warp_wait(&B->o[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u, abort_flag, a.status)
                    : warp_wait(&B->o[s], 0, abort_flag, a.status);
     __syncwarp();
     tc_fence_after();
@@ -644,7 +674,8 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
         }
         if (whole) {  // a block of 64 dims leaves while the next is staged
           fence_proxy_async_smem();
-          asm volatile("bar.sync %0, 128;" ::"r"(1 + s) : "memory");
+          if (s == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
+          else asm volatile("bar.sync 2, 128;" ::: "memory");
           if (row == 0) {
             tma_store_3d(&omap, tile + d * (128 * 128), d * 64, w.kvh * L.G + w.g0, w.q_row0 + t0);
             bulk_commit();
@@ -694,7 +725,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
   __syncthreads();
   if (warp == C::W_MMA) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, C::COLS);
   }
   if (L.split > 1) {
     __syncwarp();
@@ -770,8 +801,12 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, 1)
   }
 }
 
+// Clusters of 1, 2, 4 and 8 CTAs that the GPU holds at once, for head_dim 64, 128,
+// 256 (the same for every GPU this library runs on).
+int g_resident[3][4];
+
 template <int DH>
-cudaError_t launch(const PromptAttnArgs& a, int sm_count, cudaStream_t st) {
+cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
   using C = Cfg<DH>;
   Launch L;
   L.G = a.Hq / a.Hkv;
@@ -790,23 +825,38 @@ cudaError_t launch(const PromptAttnArgs& a, int sm_count, cudaStream_t st) {
     }
   L.n_order = n;
   int64_t units = 0;
+  double steps = 0;  // key tiles of all units
+  const int longest = (a.kv_len[L.order[0]] + C::BK - 1) / C::BK;  // of one unit
   for (int i = 0; i < n; ++i) {
     const int b = L.order[i], tok = a.cu_q[b + 1] - a.cu_q[b];
     L.work_cu[i] = (int)units;
-    units += (int64_t)((tok + L.T * C::NQ - 1) / (L.T * C::NQ)) * a.Hkv * L.hc;
+    const int64_t mine = (int64_t)((tok + L.T * C::NQ - 1) / (L.T * C::NQ)) * a.Hkv * L.hc;
+    steps += (double)mine * (a.causal ? a.kv_len[b] - 0.5 * tok : a.kv_len[b]) / C::BK + 0.5 * mine;
+    units += mine;
     if (units > 0x7fffffff / 8) return cudaErrorInvalidConfiguration;
   }
   L.work_cu[n] = (int)units;
   L.per_inv = L.per > 1 && units * L.per < ((int64_t)1 << 32) ? (uint32_t)(((1ull << 32) + L.per - 1) / L.per) : 0;
-  // Few units over long key ranges: split the keys over the CTAs of a cluster,
-  // as many as stay resident together, while a CTA keeps two tiles.  The merge
-  // costs about as much as five tiles, so halves pay for longer ranges only:
-  // 16 rows over 1016 keys 32/8/128 12.0 us split by 4, 14.6 unsplit; 400 tokens
-  // 13.7 us split by 2, 10.9 unsplit.
-  const int tiles = (a.kv_len[L.order[0]] + C::BK - 1) / C::BK;
+  // Split the keys of a unit over the CTAs of a cluster where that shortens the
+  // launch: the longest unit, or the rounds of CTAs on an SM, whichever is more,
+  // in clocks from measured costs of a key tile, of a unit's start and end, and of
+  // a merge.  (12.0 us against 14.6 unsplit for 16 rows over 1016 keys 32/8/128,
+  // split by 4; 10.8 unsplit against 13.7 split by 2 for 400 tokens.)
+  const double tile = DH == 64 ? 2000 : 2700, shared = 2400, ends = 8500;
+  double best = 0;
   L.split = 1;
-  while (L.split < 8 && units * L.split * 2 <= sm_count) L.split *= 2;
-  while (L.split > 1 && tiles < (L.split >= 4 ? 2 * L.split : 8)) L.split /= 2;
+  for (int e = 0; e < 4; ++e) {
+    const int n = 1 << e, ctas = g_resident[DH / 128][e] << e;  // at once
+    if (ctas == 0 || longest < 2 * n - 1) continue;
+    const double step = (C::CTAS == 2 && n == 1 ? shared : tile), own = ends + (n > 1 ? 6000 + 10000.0 / n : 0);
+    const double chain = own + tile * ((longest + n - 1) / n);
+    const double all = (double)((units * n + ctas - 1) / ctas) * (own + step * steps / ((double)units * n));
+    const double cost = chain > all ? chain : all;
+    if (e == 0 || cost < best) {
+      best = cost;
+      L.split = n;
+    }
+  }
 
   CUtensorMap qmap, kmap, vmap, omap;
   cudaError_t e = make_bf16_3d_map(&qmap, a.q, {DH, a.Hq, a.cu_q[a.batch]}, {DH, (long)a.q_stride}, {64, L.Gc, L.T});
@@ -822,7 +872,7 @@ cudaError_t launch(const PromptAttnArgs& a, int sm_count, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * L.split));
   cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = C::BYTES;
+  cfg.dynamicSmemBytes = L.split > 1 ? C::SPLIT_BYTES : C::BYTES;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -836,18 +886,31 @@ cudaError_t launch(const PromptAttnArgs& a, int sm_count, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int dh, int sm_count, cudaStream_t s) {
-  if (dh == 64) return launch<64>(a, sm_count, s);
-  if (dh == 128) return launch<128>(a, sm_count, s);
-  return launch<256>(a, sm_count, s);
+cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int dh, cudaStream_t s) {
+  if (dh == 64) return launch<64>(a, s);
+  if (dh == 128) return launch<128>(a, s);
+  return launch<256>(a, s);
 }
 
 template <int DH>
 static cudaError_t setup() {
+  using C = Cfg<DH>;
   cudaError_t e = cudaSuccess;
   for (auto kern : {k_prompt_attn<DH, false>, k_prompt_attn<DH, true>})
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<DH>::BYTES);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SPLIT_BYTES);
+  for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(8);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = i > 0 ? C::SPLIT_BYTES : C::BYTES;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1u << i;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaOccupancyMaxActiveClusters(&g_resident[DH / 128][i], k_prompt_attn<DH, false>, &cfg);
+  }
   return e;
 }
 
