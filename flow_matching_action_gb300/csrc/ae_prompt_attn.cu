@@ -4,8 +4,8 @@
 // T = 128 / G consecutive tokens of a sequence times its G heads (row =
 // token * G + head; T * G <= 128 rows used), so short prompts fill tiles and a
 // causal diagonal covers few keys.  One CTA works on NQ tiles of one
-// (sequence, KV head) and walks the keys in tiles of 128 with an online softmax:
-//   S = Q K^T       tcgen05, M = N = 128, fp32 in tensor memory
+// (sequence, KV head) and walks the keys in tiles of BK with an online softmax:
+//   S = Q K^T       tcgen05, M = 128, N = BK, fp32 in tensor memory
 //   P = 2^(c S - m) one thread per row; bf16 back over the S columns it read
 //   O += P V        tcgen05, P as the TMEM A operand, O stays in tensor memory
 // The exponent reference m is raised (and O, l rescaled) only when a row's
@@ -24,11 +24,14 @@
 //     fits beside Q.  8192 tokens 8/1/256: 150 us, 1830 TFLOP/s.  (Key tiles of
 //     64: 191 us, Q K^T of 64 columns is bound by reading Q from shared memory.)
 //   head_dim 64: one tile a CTA and two CTAs a SM, each in the half of tensor
-//     memory, so one's start, end and MMAs run under the other's softmax; bound
-//     by the exponentials and the latency of a softmax step.  8192 tokens
-//     12/4/64: 115 us, 895 TFLOP/s.  (Two tiles sharing K and V in one CTA: 117
-//     us, and 19.8 against 14.6 us for 64 prompts of 100 tokens; four tiles a
-//     CTA on keys of 64: 138 us.)
+//     memory, so one's start, end and MMAs run under the other's softmax; key
+//     tiles of 96, the largest of which two score buffers fit beside O, so the
+//     next Q K^T runs under this softmax too.  Bound by a softmax warp's issue and
+//     the exponentials, half of the cycles each.  8192 tokens 12/4/64: 101 us,
+//     1020 TFLOP/s.  (Key tiles of 128, one score buffer: 115 us, prompts of one
+//     to 4097 tokens 40.6 against 34.7 us; 100 tokens, which that holds in one
+//     tile, 14.6 against 15.0 us for 64 of them.  Two tiles sharing K and V in one
+//     CTA: 117 us; four on keys of 64: 138 us.)
 // What the MMAs need most is an issue thread that never waits: they are issued
 // under elect.sync on warp-uniform operands (a plain lane test costs 75 clocks
 // per MMA in register moves: 6.7 ms for the 32768 tokens), and both next slots
@@ -61,9 +64,9 @@ constexpr float kRaise = 8.f;  // log2: raise the exponent reference past this
 template <int DH>
 struct Cfg {
   static constexpr int NQ = DH == 128 ? 2 : 1;     // query tiles of a CTA
-  static constexpr int SB = DH == 256 ? 2 : 1;     // score buffers of a query tile
+  static constexpr int SB = NQ == 1 ? 2 : 1;     // score buffers of a query tile
   static constexpr int CTAS = DH == 64 ? 2 : 1;    // resident a SM
-  static constexpr int BK = 128;                   // keys of a tile
+  static constexpr int BK = DH == 64 ? 96 : 128;                   // keys of a tile
   static constexpr int DB = DH / 64;               // 64-dim blocks of a row
   // a ring slot holds a K or V tile; at head_dim 256 half of one: all keys of half
   // the dims of K, all dims of half the keys of V
@@ -74,10 +77,10 @@ struct Cfg {
   static constexpr int QBYTES = 128 * DH * 2;      // bytes of a query tile
   // threads: the softmax warpgroups, then one of which two warps work (loads,
   // MMAs).  It hands registers to the others where the launch's would not do:
-  // 104 + 2 * 200 = 3 * 168 (NQ = 2), 72 + 184 = 2 * 128 (two CTAs a SM).
+  // 104 + 2 * 200 = 3 * 168 (NQ = 2), 96 + 160 = 2 * 128 (two CTAs a SM).
   static constexpr int THREADS = NQ * 128 + 128;
   static constexpr bool TRADE = NQ == 2 || CTAS == 2;
-  static constexpr int REGS_AUX = NQ == 2 ? 104 : 72, REGS_MAX = NQ == 2 ? 200 : 184;
+  static constexpr int REGS_AUX = NQ == 2 ? 104 : 96, REGS_MAX = NQ == 2 ? 200 : 160;
   static constexpr int W_LOAD = NQ * 4, W_MMA = NQ * 4 + 1;
   // shared memory, from a 1024-byte boundary
   static constexpr int RING = NQ * QBYTES;
@@ -256,6 +259,77 @@ __device__ __forceinline__ Unit find_unit(const PromptAttnArgs& a, const Launch&
   w.g0 = (h - w.kvh * L.hc) * L.Gc;
   w.tok0 = t * L.T * Cfg<DH>::NQ;
   return w;
+}
+
+// Rank r of P CTAs merges its share of the rows in use: 16-byte pieces of the
+// partials, 16 in flight a thread, the first ones under the computation of the
+// weights 2^(m_p - m) / l of every split.  Bound by remote shared memory (15 bytes
+// a clock measured with all of them in flight), so rows that hold no query are
+// left out: 16 tokens over 1016 keys 32/8/128 9.8 us, 12.4 with them.
+template <int DH, int P>
+__device__ __forceinline__ void merge_rows(const PromptAttnArgs& a, const Launch& L, const Unit& w, uint8_t* smem,
+                                           int rank) {
+  using C = Cfg<DH>;
+  constexpr int PER = DH / 4, UN = 16 / P;
+  const int rows0 = max(0, min(L.T, w.n_new - w.tok0)) * L.Gc;
+  const int rows = rows0 + (C::NQ == 2 ? max(0, min(L.T, w.n_new - w.tok0 - L.T)) * L.Gc : 0);
+  const int i_lo = rows * rank / P, share = rows * (rank + 1) / P - i_lo;
+  auto tile_row = [&](int i) { return i_lo + i < rows0 ? i_lo + i : 128 + i_lo + i - rows0; };
+  const uint32_t base = smem_u32(smem), ml = smem_u32(smem + C::ML);
+  float* wt = reinterpret_cast<float*>(smem + C::WT);  // [share][P]
+  uint32_t peer[P];
+#pragma unroll
+  for (int p = 0; p < P; ++p) peer[p] = mapa(base, p);
+  float4 v[UN][P];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int e = 0; e < UN; ++e) {
+      const int i = i0 + e * C::THREADS, r = tile_row(i / PER), q = i % PER;
+      if (i >= share * PER) break;
+      const uint32_t off = r * (DH * 4) + ((q ^ (r & 7)) << 4);
+#pragma unroll
+      for (int p = 0; p < P; ++p) v[e][p] = ld_cluster_f4(peer[p] + off);
+    }
+  };
+  load(threadIdx.x);
+  for (int i = threadIdx.x; i < share; i += C::THREADS) {
+    const int r = tile_row(i);
+    float2 x[P];
+    float m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int p = 0; p < P; ++p) x[p] = ld_cluster_f2(mapa(ml + r * 8, p));
+#pragma unroll
+    for (int p = 0; p < P; ++p) m = fmaxf(m, x[p].x);
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      x[p].x = x[p].y > 0.f ? ex2_fast(x[p].x - m) : 0.f;
+      l += x[p].x * x[p].y;
+    }
+#pragma unroll
+    for (int p = 0; p < P; ++p) wt[i * P + p] = l > 0.f ? x[p].x / l : 0.f;
+  }
+  __syncthreads();
+  for (int i0 = threadIdx.x; i0 < share * PER; i0 += UN * C::THREADS) {
+    if (i0 != (int)threadIdx.x) load(i0);
+#pragma unroll
+    for (int e = 0; e < UN; ++e) {
+      const int i = i0 + e * C::THREADS, r = tile_row(i / PER), q = i % PER;
+      const int s = r >> 7, rr = r & 127;
+      const int tok = divide(rr, L.Gc, L.gc_inv), g = w.g0 + rr - tok * L.Gc;
+      if (i >= share * PER || g >= L.G) continue;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const float f = wt[(i / PER) * P + p];
+        o.x += f * v[e][p].x;
+        o.y += f * v[e][p].y;
+        o.z += f * v[e][p].z;
+        o.w += f * v[e][p].w;
+      }
+      *reinterpret_cast<uint2*>(a.out + (int64_t)(w.q_row0 + w.tok0 + s * L.T + tok) * a.out_stride +
+                                (int64_t)(w.kvh * L.G + g) * DH + 4 * q) = make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
+    }
+  }
 }
 
 // MASKED: the call has a key mask.
@@ -645,7 +719,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
                    : warp_wait(&B->o[s], 0, abort_flag, a.status);
     __syncwarp();
     tc_fence_after();
-    if (ok && L.split == 1) {
+    if (L.split == 1) {
       // Rows through shared memory, over the query tile whose products are done
       // (its layout), then out by TMA; a tile cut short by the sequence's end (or
       // the group's) in runs of whole rows by its threads.
@@ -676,7 +750,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
           fence_proxy_async_smem();
           if (s == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
           else asm volatile("bar.sync 2, 128;" ::: "memory");
-          if (row == 0) {
+          if (row == 0 && ok) {
             tma_store_3d(&omap, tile + d * (128 * 128), d * 64, w.kvh * L.G + w.g0, w.q_row0 + t0);
             bulk_commit();
           }
@@ -684,7 +758,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
       }
       if (whole) {
         if (row == 0) bulk_wait_read_all();
-      } else {
+      } else if (ok) {
         __syncwarp();  // a warp stores the 32 rows it wrote
         constexpr int CPR = DH / 8, RPI = 32 / CPR;  // pieces of a row; rows an instruction
         const int r0 = 32 * (warp & 3) + lane / CPR, ch = lane % CPR;
@@ -736,65 +810,9 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
     asm volatile("" : "+r"(bx));
     const Unit w = find_unit<DH>(a, L, bx / L.split);
     const int rank = (int)cluster_rank();
-    // rank r merges its share of the rows: the weight 2^(m_p - m) / l of every
-    // split first, then DH / 4 four-dim pieces a row
-    const int share = NQ * 128 / L.split;
-    constexpr int PER = DH / 4, UN = 2;
-    const uint32_t base = smem_u32(smem), ml = smem_u32(smem + C::ML);
-    float* wt = reinterpret_cast<float*>(smem + C::WT);  // [share][split]
-    for (int i = threadIdx.x; i < share; i += C::THREADS) {
-      const int r = rank * share + i;
-      float2 x[8];
-      float m = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        x[p] = p < L.split ? ld_cluster_f2(mapa(ml + r * 8, p)) : make_float2(-INFINITY, 0.f);
-        m = fmaxf(m, x[p].x);
-      }
-#pragma unroll
-      for (int p = 0; p < 8; ++p) {
-        x[p].x = x[p].y > 0.f ? ex2_fast(x[p].x - m) : 0.f;
-        l += x[p].x * x[p].y;
-      }
-#pragma unroll
-      for (int p = 0; p < 8; ++p)
-        if (p < L.split) wt[i * L.split + p] = l > 0.f ? x[p].x / l : 0.f;
-    }
-    __syncthreads();
-    uint32_t peer[8];
-#pragma unroll
-    for (int p = 0; p < 8; ++p) peer[p] = mapa(base, p < L.split ? p : 0);
-    for (int i0 = threadIdx.x; i0 < share * PER; i0 += UN * C::THREADS) {
-      float4 v[UN][8];  // every split's piece in flight at once
-#pragma unroll
-      for (int e = 0; e < UN; ++e) {
-        const int i = min(i0 + e * C::THREADS, share * PER - 1), r = rank * share + i / PER, q = i % PER;
-#pragma unroll
-        for (int p = 0; p < 8; ++p)
-          v[e][p] = p < L.split ? ld_cluster_f4(peer[p] + r * (DH * 4) + ((q ^ (r & 7)) << 4))
-                                : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
-#pragma unroll
-      for (int e = 0; e < UN; ++e) {
-        const int i = i0 + e * C::THREADS, r = rank * share + i / PER, q = i % PER;
-        const int s = r >> 7, rr = r & 127;
-        const int tok = divide(rr, L.Gc, L.gc_inv), g = w.g0 + rr - tok * L.Gc;
-        const int t = w.tok0 + s * L.T + tok;
-        if (i >= share * PER || tok >= L.T || t >= w.n_new || g >= L.G) continue;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int p = 0; p < 8; ++p)
-          if (p < L.split) {
-            const float f = wt[(i / PER) * L.split + p];
-            o.x += f * v[e][p].x;
-            o.y += f * v[e][p].y;
-            o.z += f * v[e][p].z;
-            o.w += f * v[e][p].w;
-          }
-        *reinterpret_cast<uint2*>(a.out + (int64_t)(w.q_row0 + t) * a.out_stride + (int64_t)(w.kvh * L.G + g) * DH +
-                                  4 * q) = make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
-      }
-    }
+    if (L.split == 2) merge_rows<DH, 2>(a, L, w, smem, rank);
+    else if (L.split == 4) merge_rows<DH, 4>(a, L, w, smem, rank);
+    else merge_rows<DH, 8>(a, L, w, smem, rank);
     __syncthreads();
     cluster_arrive();  // no CTA leaves while a peer reads its partials
     cluster_wait();
@@ -842,7 +860,7 @@ cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
   // in clocks from measured costs of a key tile, of a unit's start and end, and of
   // a merge.  (12.0 us against 14.6 unsplit for 16 rows over 1016 keys 32/8/128,
   // split by 4; 10.8 unsplit against 13.7 split by 2 for 400 tokens.)
-  const double tile = DH == 64 ? 2000 : 2700, shared = 2400, ends = 8500;
+  const double tile = DH == 64 ? 1500 : 2700, shared = 1800, ends = 8500;
   double best = 0;
   L.split = 1;
   for (int e = 0; e < 4; ++e) {
