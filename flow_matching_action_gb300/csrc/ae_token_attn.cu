@@ -21,6 +21,12 @@
 // (remote shared memory), and after one cluster barrier each owner merges its
 // dims: one launch, no workspace, sums in a fixed order.  The ranges follow the
 // lengths on the device, whatever the lengths of the capture were.
+// Bound by the bytes of K and V where requests fill the GPU: 64 of 8k keys
+// 32/8/128 293 us, 7.2 TB/s.  Few or short requests are bound by a launch, the
+// first loads, and the two merges: 712 keys 8/1/256 5.5 us; twelve requests of up
+// to 2048 keys, a camera slot masked, 7.7 us (1.4 TB/s).
+// Scores, statistics and O are fp32; weights are rounded to bf16 because the
+// tensor cores multiply bf16 (an error of at most 2^-8 of each term), O once.
 #include <math.h>
 
 #include "ae_internal.h"
