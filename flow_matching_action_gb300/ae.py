@@ -252,24 +252,30 @@ def _load_dtypes():
     _BF16, _I32, _I64, _U8 = torch.bfloat16, torch.int32, torch.int64, torch.uint8
 
 
-def _rows(name: str, t, width: int, rows: int = -1):
-    """(pointer, row stride) of a bf16 CUDA tensor [rows, width] whose rows are contiguous."""
+def _current_device() -> int:
+    import torch
+    return torch.cuda.current_device()
+
+
+def _rows(name: str, t, width: int, device: int, rows: int = -1):
+    """(pointer, row stride, rows) of a bf16 tensor [rows, width] on the device whose rows are contiguous."""
     shape, step = t.shape, t.stride()
     if len(shape) != 2 or shape[1] != width or (rows >= 0 and shape[0] != rows):
         raise ValueError(f"{name}: shape {tuple(shape)}, expected [{'rows' if rows < 0 else rows}, {width}]")
-    if t.dtype is not _BF16 or not t.is_cuda:
-        raise ValueError(f"{name}: expected a bf16 CUDA tensor, got {t.dtype} on {t.device}")
+    if t.dtype is not _BF16 or t.get_device() != device:
+        raise ValueError(f"{name}: expected a bf16 tensor on cuda:{device}, got {t.dtype} on {t.device}")
     if step[1] != 1:
         raise ValueError(f"{name}: the elements of a row must be contiguous")
-    return t.data_ptr(), step[0] if shape[0] > 1 else width  # one row has no stride
+    n = shape[0]
+    return t.data_ptr(), step[0] if n > 1 else width, n  # one row has no stride
 
 
-def _vec(name: str, t, dtype, n: int) -> int:
-    """Pointer of a contiguous CUDA tensor of n elements, 0 for None."""
+def _vec(name: str, t, dtype, device: int, n: int) -> int:
+    """Pointer of a contiguous tensor of n elements on the device, 0 for None."""
     if t is None:
         return 0
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != n:
-        raise ValueError(f"{name}: expected {n} contiguous {dtype} elements on the GPU, got {tuple(t.shape)} "
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name}: expected {n} contiguous {dtype} elements on cuda:{device}, got {tuple(t.shape)} "
                          f"{t.dtype} on {t.device}")
     return t.data_ptr()
 
@@ -375,6 +381,8 @@ class ActionExpert:
         _load_dtypes()
         self._q_dim, self._kv_dim = dims.n_q_heads * dims.head_dim, dims.n_kv_heads * dims.head_dim
         self.ctx = ae_create(self.config, self._wstruct, max_batch, max_prefix_rows, stream)
+        self._device = _current_device()  # the context's, as ae_create takes it
+        self._axis_array = ctypes.c_uint8 * (dims.head_dim // 2)
         self._bound = None
 
     def bind_prefix(self, prefix_k, prefix_v, cu_lens, prefix_mask=None):
@@ -400,20 +408,20 @@ class ActionExpert:
         positions int32 [tokens] or [axes, tokens]; kv_rows int64 [tokens] or None; pair_axis bytes or a
         sequence of dh / 2 axes; pair_freq a sequence of dh / 2 frequencies.
         """
-        qd, kvd, dh = self._q_dim, self._kv_dim, self.dims.head_dim
-        n, cache_rows = qkv.shape[0], k_cache.shape[0]
+        qd, kvd, dh, dev = self._q_dim, self._kv_dim, self.dims.head_dim, self._device
         axes = positions.shape[0] if positions.dim() == 2 else 1
         pair_axis, freq = _pairs(pair_axis, pair_freq, dh // 2)
-        x, x_stride = _rows("qkv", qkv, qd + 2 * kvd)
-        q, q_stride = _rows("q_out", q_out, qd, n)
-        k, k_stride = _rows("k_cache", k_cache, kvd)
-        v, v_stride = _rows("v_cache", v_cache, kvd, cache_rows)
+        x, x_stride, n = _rows("qkv", qkv, qd + 2 * kvd, dev)
+        q, q_stride, _ = _rows("q_out", q_out, qd, dev, n)
+        k, k_stride, cache_rows = _rows("k_cache", k_cache, kvd, dev)
+        v, v_stride, _ = _rows("v_cache", v_cache, kvd, dev, cache_rows)
         if v_stride != k_stride:
             raise ValueError("k_cache and v_cache have different row strides")
-        axis = None if pair_axis is None else (ctypes.c_uint8 * (dh // 2)).from_buffer_copy(pair_axis)
+        axis = None if pair_axis is None else self._axis_array.from_buffer_copy(pair_axis)
         _call_packed("ae_qk_norm_rope", self.ctx, _ROPE_ARGS.pack(
-            n, axes, x, x_stride, _vec("q_norm", q_norm, _BF16, dh), _vec("k_norm", k_norm, _BF16, dh), norm_offset,
-            _vec("positions", positions, _I32, axes * n), _addr(axis), _addr(freq), _vec("kv_rows", kv_rows, _I64, n), cache_rows, q, q_stride, k, v, k_stride))
+            n, axes, x, x_stride, _vec("q_norm", q_norm, _BF16, dev, dh), _vec("k_norm", k_norm, _BF16, dev, dh),
+            norm_offset, _vec("positions", positions, _I32, dev, axes * n), _addr(axis), _addr(freq),
+            _vec("kv_rows", kv_rows, _I64, dev, n), cache_rows, q, q_stride, k, v, k_stride))
 
     def prompt_attention(self, q, k, v, cu_q, kv_row0=None, kv_len=None, key_mask=None, causal: bool = True,
                          scale: float = 0.0, out=None):
@@ -430,18 +438,18 @@ class ActionExpert:
         for name, x in (("kv_row0", row0), ("kv_len", lens)):
             if x is not None and len(x) != batch:
                 raise ValueError(f"{name}: {len(x)} entries for {batch} sequences")
-        rows, cache_rows = q.shape[0], k.shape[0]
+        dev = self._device
+        qp, q_stride, rows = _rows("q", q, self._q_dim, dev)
         if rows < cu[batch]:
             raise ValueError(f"q: {rows} rows, cu_q ends at {cu[batch]}")
-        qp, q_stride = _rows("q", q, self._q_dim)
-        kp, k_stride = _rows("k", k, self._kv_dim)
-        vp, v_stride = _rows("v", v, self._kv_dim, cache_rows)
+        kp, k_stride, cache_rows = _rows("k", k, self._kv_dim, dev)
+        vp, v_stride, _ = _rows("v", v, self._kv_dim, dev, cache_rows)
         if v_stride != k_stride:
             raise ValueError("k and v have different row strides")
-        op, o_stride = _rows("out", out, self._q_dim, rows)
+        op, o_stride, _ = _rows("out", out, self._q_dim, dev, rows)
         _call_packed("ae_prompt_attention", self.ctx, _PROMPT_ARGS.pack(
             batch, 1 if causal else 0, _addr(cu), _addr(row0), _addr(lens), cache_rows, qp, q_stride, kp, vp, k_stride,
-            _vec("key_mask", key_mask, _U8, cache_rows), scale, op, o_stride))
+            _vec("key_mask", key_mask, _U8, dev, cache_rows), scale, op, o_stride))
         return out
 
     def token_attention(self, q, k, v, kv_row0, kv_len, max_len: int, key_mask=None, scale: float = 0.0, out=None):
@@ -452,16 +460,16 @@ class ActionExpert:
         """
         if out is None:
             out = q.new_empty(q.shape)
-        n, cache_rows = q.shape[0], k.shape[0]
-        qp, q_stride = _rows("q", q, self._q_dim)
-        kp, k_stride = _rows("k", k, self._kv_dim)
-        vp, v_stride = _rows("v", v, self._kv_dim, cache_rows)
+        dev = self._device
+        qp, q_stride, n = _rows("q", q, self._q_dim, dev)
+        kp, k_stride, cache_rows = _rows("k", k, self._kv_dim, dev)
+        vp, v_stride, _ = _rows("v", v, self._kv_dim, dev, cache_rows)
         if v_stride != k_stride:
             raise ValueError("k and v have different row strides")
-        op, o_stride = _rows("out", out, self._q_dim, n)
+        op, o_stride, _ = _rows("out", out, self._q_dim, dev, n)
         _call_packed("ae_token_attention", self.ctx, _TOKEN_ARGS.pack(
-            n, max_len, _vec("kv_row0", kv_row0, _I64, n), _vec("kv_len", kv_len, _I32, n), cache_rows, qp, q_stride,
-            kp, vp, k_stride, _vec("key_mask", key_mask, _U8, cache_rows), scale, op, o_stride))
+            n, max_len, _vec("kv_row0", kv_row0, _I64, dev, n), _vec("kv_len", kv_len, _I32, dev, n), cache_rows, qp,
+            q_stride, kp, vp, k_stride, _vec("key_mask", key_mask, _U8, dev, cache_rows), scale, op, o_stride))
         return out
 
     def prefill_prompts(self, embeddings, cu_lens, positions, out_k, out_v, causal: bool = True, token_mask=None,
@@ -471,17 +479,17 @@ class ActionExpert:
         embeddings [total, width] bf16; positions int32 [total] or [axes, total]; out_k / out_v
         [layers, total, Hkv dh] bf16; q_norm / k_norm one bf16 [dh] tensor a layer.
         """
-        d = self.dims
+        d, dev = self.dims, self._device
         cu = _host_array(ctypes.c_int32, cu_lens)
         n = embeddings.shape[0]
         if cu[len(cu) - 1] != n:
             raise ValueError(f"embeddings: {n} rows, cu_lens ends at {cu[len(cu) - 1]}")
         a = ae_prefill_prompts_args()
         a.batch, a.causal, a.cu_lens = len(cu) - 1, 1 if causal else 0, _addr(cu)
-        a.embeddings = _vec("embeddings", embeddings, _BF16, n * d.width)
-        a.token_mask = _vec("token_mask", token_mask, _U8, n)
+        a.embeddings = _vec("embeddings", embeddings, _BF16, dev, n * d.width)
+        a.token_mask = _vec("token_mask", token_mask, _U8, dev, n)
         a.n_axes = positions.shape[0] if positions.dim() == 2 else 1
-        a.positions = _vec("positions", positions, _I32, a.n_axes * n)
+        a.positions = _vec("positions", positions, _I32, dev, a.n_axes * n)
         a.pair_axis, freq = _pairs(pair_axis, pair_freq, d.head_dim // 2)
         a.pair_freq = _addr(freq)
         norms = []
@@ -489,11 +497,11 @@ class ActionExpert:
             if w is not None and len(w) != d.layers:
                 raise ValueError(f"{name}: {len(w)} tensors for {d.layers} layers")
             norms.append(None if w is None else (ctypes.c_void_p * d.layers)(
-                *[_vec(name, x, _BF16, d.head_dim) for x in w]))
+                *[_vec(name, x, _BF16, dev, d.head_dim) for x in w]))
         a.q_norm, a.k_norm = _addr(norms[0]), _addr(norms[1])
         a.norm_offset = norm_offset
-        a.out_k = _vec("out_k", out_k, _BF16, d.layers * n * d.kv_dim)
-        a.out_v = _vec("out_v", out_v, _BF16, d.layers * n * d.kv_dim)
+        a.out_k = _vec("out_k", out_k, _BF16, dev, d.layers * n * d.kv_dim)
+        a.out_v = _vec("out_v", out_v, _BF16, dev, d.layers * n * d.kv_dim)
         ae_prefill_prompts(self.ctx, a)
 
     def sample(self, noise, n_steps: int, out=None):

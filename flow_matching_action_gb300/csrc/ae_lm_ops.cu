@@ -102,12 +102,18 @@ ae_status launched(ae_ctx* c, cudaError_t e, const char* op) {
 namespace ae {
 
 uint64_t turn_fraction(double radians) {
-  const double turns = radians * 0.15915494309189533577;  // 1 / (2 pi)
-  const double frac = turns - floor(turns);               // whole turns drop out
+  // 1 / (2 pi) as the sum of two doubles: the product is good to 2^-64 of a turn
+  // for every frequency up to 2^40
+  const double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
+  const double turns = radians * hi;
+  const double frac = turns - floor(turns);  // whole turns drop out; exact
+  double rest = fma(radians, hi, -turns) + radians * lo;
+  rest -= rint(rest);
+  if (rest >= 0.5) rest -= 1.0;
   // frac in [0, 1]; 2^64 itself wraps to 0
-  const double hi = floor(frac * 4294967296.0);
-  const double lo = (frac * 4294967296.0 - hi) * 4294967296.0;
-  return ((uint64_t)hi << 32) + (uint64_t)lo;
+  const double top = floor(frac * 4294967296.0);
+  const double low = (frac * 4294967296.0 - top) * 4294967296.0;
+  return ((uint64_t)top << 32) + (uint64_t)low + (uint64_t)(int64_t)(rest * 18446744073709551616.0);
 }
 
 }  // namespace ae
@@ -119,7 +125,7 @@ ae_status ae_qk_norm_rope(ae_ctx* c, const ae_qk_norm_rope_args* p) {
   const char* op = "ae_qk_norm_rope";
   AE_TRY(check_context(c, p, op));
   const ae::Dims& d = c->d;
-  if (p->tokens < 0) return fail(c, AE_ERR_SHAPE, "tokens %d < 0", p->tokens);
+  if (p->tokens < 0 || p->tokens > 0x7fff0000) return fail(c, AE_ERR_SHAPE, "tokens %d outside 0..%d", p->tokens, 0x7fff0000);
   if (!isfinite(p->norm_offset)) return fail(c, AE_ERR_INVALID_ARG, "norm_offset must be finite");
   AE_TRY(check_cache_rows(c, p->cache_rows));
   AE_TRY(check_rotation(c, p->n_axes, p->pair_axis, p->pair_freq));

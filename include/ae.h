@@ -288,11 +288,12 @@ AE_API ae_status ae_prefill(ae_ctx* ctx, int batch, const void* embeddings, void
  *   phi(j)        = positions[pair_axis[j]][t] * pair_freq[j],   j < dh/2
  *   out[j]        = y[j] cos phi - y[j + dh/2] sin phi
  *   out[j + dh/2] = y[j + dh/2] cos phi + y[j] sin phi
- * in fp32, rounded once to bf16 (the angle is reduced exactly: every int32
- * position is as accurate as small ones).  Values are copied.
+ * in fp32, rounded once to bf16 (the angle is taken modulo one turn in 64-bit
+ * integers: every int32 position is as accurate as small ones, for frequencies
+ * up to 2^30).  Values are copied.
  */
 typedef struct {
-  int tokens;                /* >= 0                                             */
+  int tokens;                /* 0 .. 2^31 - 2^16                                 */
   int n_axes;                /* rows of positions, 1..AE_MAX_AXES                */
   const void* qkv;           /* device bf16 [tokens][q heads | k heads | v heads] */
   int64_t qkv_stride;

@@ -135,6 +135,31 @@ def test_rope_far_positions_and_given_frequencies(experts):
     assert (np.abs(got - ref) <= tol).all()
 
 
+def test_rope_frequencies_above_one_turn(experts):
+    """Frequencies of many turns a position, at far positions: the angle modulo one turn in exact
+    arithmetic (80 digits of pi).  Its fp32 sine and cosine are good to 2^-18."""
+    import torch
+    from fractions import Fraction
+    two_pi = 2 * Fraction(314159265358979323846264338327950288419716939937510582097494459230781640628620899, 10 ** 80)
+    hq, hkv, dh = 4, 1, 64
+    ex, g = experts(hq, hkv, dh), generator(4)
+    positions = [1, -7, 2 ** 31 - 1, -2 ** 31, 1234567891]
+    pos = torch.tensor([positions], dtype=torch.int32, device="cuda")
+    half = dh // 2
+    freq = [(-1) ** j * 1.0001 * 1.9 ** j for j in range(half)]
+    n = len(positions)
+    qkv = normal(g, n, (hq + 2 * hkv) * dh)
+    q = torch.empty((n, hq * dh), dtype=torch.bfloat16, device="cuda")
+    k = torch.empty((n, hkv * dh), dtype=torch.bfloat16, device="cuda")
+    ex.qk_norm_rope(qkv, pos, q, k, torch.empty_like(k), pair_freq=freq)
+    ex.synchronize()
+    phi = np.array([[float(p * Fraction(f) / two_pi % 1) for f in freq] for p in positions])[:, None] * 2 * np.pi
+    x = f64(qkv).reshape(n, hq + 2 * hkv, dh)[:, :hq]
+    lo, hi = x[..., :half], x[..., half:]
+    ref = np.concatenate([lo * np.cos(phi) - hi * np.sin(phi), hi * np.cos(phi) + lo * np.sin(phi)], -1)
+    check_rope(f64(q).reshape(n, hq, dh), ref, "q")
+
+
 def test_rope_in_place_strides_and_skipped_rows(experts):
     """q written over the projection's own columns, wide rows, tokens without a cache row, a row
     beyond the cache reported and skipped."""
@@ -270,6 +295,37 @@ def test_prompt_attention_masked_key_ranges_of_any_length(experts):
     for dh, n in ((256, 300000), (64, 70000)):
         run_prompt(experts(8, 1, 256) if dh == 256 else experts(4, 1, 64), 8 if dh == 256 else 4, 1, dh, [5], [n - 5],
                    masked=lambda i, m: (i // 100) % 3 != 1 and i % 7 != 0, gap=1, seed=n)
+
+
+def test_prompt_attention_masked_keys_beyond_the_list(experts):
+    """One CTA's key range longer than its tile list: 64 one-token sequences that share 60000 masked
+    rows fill the GPU, so their keys are not split."""
+    import torch
+    hq, hkv, dh, rows, batch = 12, 4, 64, 60000, 64
+    ex, g = experts(hq, hkv, dh), generator(60)
+    q, k, v = normal(g, batch, hq * dh), normal(g, rows, hkv * dh), normal(g, rows, hkv * dh)
+    mask = (torch.rand(rows, generator=g, device="cuda") < 0.5).to(torch.uint8)
+    mask[1000:3000] = 0
+    lens = [rows - 37 * (b % 5) for b in range(batch)]
+    cu, row0 = list(range(batch + 1)), [0] * batch
+    ref, mag = lm_ops.packed_attention(f64(q), f64(k), f64(v), hq, hkv, cu, row0, lens, mask.cpu().numpy())
+    k[mask == 0] = float("nan")
+    v[mask == 0] = float("nan")
+    out = ex.prompt_attention(q, k, v, cu, row0, lens, key_mask=mask)
+    ex.synchronize()
+    check_attention(f64(out), ref, mag)
+
+
+@pytest.mark.parametrize("hq,hkv,dh", [(4, 1, 64), (12, 4, 64), (6, 6, 64), (8, 1, 256), (32, 8, 128)])
+@pytest.mark.parametrize("keys", [95, 96, 97, 191, 192, 193, 288, 385])
+def test_prompt_attention_key_tile_ends(experts, hq, hkv, dh, keys):
+    """Lengths around whole key tiles (96 keys at head_dim 64, 128 above), causal diagonals and masks
+    that end at them."""
+    ex = experts(hq, hkv, dh)
+    run_prompt(ex, hq, hkv, dh, [keys, 3], [0, keys - 3], gap=2, seed=keys)
+    run_prompt(ex, hq, hkv, dh, [2, 50], [keys - 2, keys], gap=1, seed=keys + 1, causal=False)
+    for cut in (lambda i, m: i < 96, lambda i, m: i >= 96, lambda i, m: not 96 <= i < 192, lambda i, m: i == m - 1):
+        run_prompt(ex, hq, hkv, dh, [4, 30], [keys - 4, keys - 30], masked=cut, gap=1, seed=keys + 2)
 
 
 @pytest.mark.parametrize("std,scale", [(30.0, 0.0), (1.0, 3.0), (1e-3, 0.0), (1.0, 1e-4)])
@@ -617,3 +673,23 @@ def test_binding_refuses_wrong_tensors(experts):
         args.update(bad)
         with pytest.raises(ValueError):
             ex.prompt_attention(**args)
+
+
+def test_binding_refuses_tensors_of_another_device(experts):
+    """A tensor's device index is compared with the context's (here a context that says it lives
+    elsewhere: one GPU is enough)."""
+    import torch
+    hq, hkv, dh = 4, 1, 64
+    ex, g = experts(hq, hkv, dh), generator(41)
+    q, k, v = normal(g, 2, hq * dh), normal(g, 2, dh), normal(g, 2, dh)
+    ex._device += 1
+    try:
+        with pytest.raises(ValueError, match="cuda:"):
+            ex.prompt_attention(q, k, v, [0, 2])
+        with pytest.raises(ValueError, match="cuda:"):
+            ex.token_attention(q, k, v, torch.zeros(2, dtype=torch.int64, device="cuda"),
+                               torch.ones(2, dtype=torch.int32, device="cuda"), 2)
+        with pytest.raises(ValueError, match="cuda:"):
+            ex.qk_norm_rope(normal(g, 2, (hq + 2 * hkv) * dh), torch.zeros(2, dtype=torch.int32, device="cuda"), q, k, v)
+    finally:
+        ex._device -= 1

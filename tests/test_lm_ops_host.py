@@ -180,3 +180,7 @@ def test_packed_arguments_have_the_structs_layout(packed, fields):
         else:
             got = getattr(s, name)
         assert got == v, name
+
+
+def test_rope_token_counts_a_launch_cannot_index(make_context):
+    refused(ae.ae_qk_norm_rope, make_context(), rope_args(tokens=2 ** 31 - 1, cache_rows=0x7fffff00), SHAPE)
