@@ -47,7 +47,10 @@
 // since 0 * NaN would reach every row.
 // Few query rows over many keys leave SMs idle: the key tiles are then split
 // over the CTAs of a cluster, which exchange fp32 partials through distributed
-// shared memory (no workspace, one launch, sums in rank order).
+// shared memory (no workspace, one launch, sums in rank order).  SMs that are
+// still idle take half of the value dims each (the scores twice, the rest once):
+// the P V, the output and the merge of a CTA are halved.  16 tokens over 4080 keys
+// 8/1/256: 12.3 us against 15.2 with whole rows; a prompt of 50: 7.3 against 7.5.
 #include <math.h>
 
 #include "ae_internal.h"
@@ -68,6 +71,7 @@ struct Cfg {
   static constexpr int CTAS = DH == 64 ? 2 : 1;    // resident a SM
   static constexpr int BK = DH == 64 ? 96 : 128;                   // keys of a tile
   static constexpr int DB = DH / 64;               // 64-dim blocks of a row
+  static constexpr int LOG_DIMS = DH == 64 ? 6 : (DH == 128 ? 7 : 8);
   // a ring slot holds a K or V tile; at head_dim 256 half of one: all keys of half
   // the dims of K, all dims of half the keys of V
   static constexpr int PARTS = DH == 256 ? 2 : 1;
@@ -79,6 +83,7 @@ struct Cfg {
   // MMAs).  It hands registers to the others where the launch's would not do:
   // 104 + 2 * 200 = 3 * 168 (NQ = 2), 96 + 160 = 2 * 128 (two CTAs a SM).
   static constexpr int THREADS = NQ * 128 + 128;
+  static constexpr bool VS = DH > 64;              // the value dims may be halved
   static constexpr bool TRADE = NQ == 2 || CTAS == 2;
   static constexpr int REGS_AUX = NQ == 2 ? 104 : 96, REGS_MAX = NQ == 2 ? 200 : 160;
   static constexpr int W_LOAD = NQ * 4, W_MMA = NQ * 4 + 1;
@@ -105,6 +110,7 @@ struct Launch {
   int per;                           // units of one token range: KV heads x head chunks
   uint32_t per_inv, gc_inv;          // ceil(2^32 / per), ceil(2^32 / Gc)
   int split;                         // CTAs of a cluster
+  int vs;                            // 2: each half of the value dims is another CTA's (cluster's)
   int work_cu[AE_MAX_BATCH + 1];     // first work unit of the i-th sequence, longest first
   uint8_t order[AE_MAX_BATCH];
 };
@@ -268,9 +274,10 @@ __device__ __forceinline__ Unit find_unit(const PromptAttnArgs& a, const Launch&
 // left out: 16 tokens over 1016 keys 32/8/128 9.8 us, 12.4 with them.
 template <int DH, int P>
 __device__ __forceinline__ void merge_rows(const PromptAttnArgs& a, const Launch& L, const Unit& w, uint8_t* smem,
-                                           int rank) {
+                                           int rank, int half) {
   using C = Cfg<DH>;
-  constexpr int PER = DH / 4, UN = 16 / P;
+  constexpr int UN = 16 / P;
+  const int shift = C::LOG_DIMS - 1 - L.vs, per = 1 << shift;  // pieces of a row
   const int rows0 = max(0, min(L.T, w.n_new - w.tok0)) * L.Gc;
   const int rows = rows0 + (C::NQ == 2 ? max(0, min(L.T, w.n_new - w.tok0 - L.T)) * L.Gc : 0);
   const int i_lo = rows * rank / P, share = rows * (rank + 1) / P - i_lo;
@@ -284,8 +291,8 @@ __device__ __forceinline__ void merge_rows(const PromptAttnArgs& a, const Launch
   auto load = [&](int i0) {
 #pragma unroll
     for (int e = 0; e < UN; ++e) {
-      const int i = i0 + e * C::THREADS, r = tile_row(i / PER), q = i % PER;
-      if (i >= share * PER) break;
+      const int i = i0 + e * C::THREADS, r = tile_row(i >> shift), q = i & (per - 1);
+      if (i >= share << shift) break;
       const uint32_t off = r * (DH * 4) + ((q ^ (r & 7)) << 4);
 #pragma unroll
       for (int p = 0; p < P; ++p) v[e][p] = ld_cluster_f4(peer[p] + off);
@@ -309,25 +316,25 @@ __device__ __forceinline__ void merge_rows(const PromptAttnArgs& a, const Launch
     for (int p = 0; p < P; ++p) wt[i * P + p] = l > 0.f ? x[p].x / l : 0.f;
   }
   __syncthreads();
-  for (int i0 = threadIdx.x; i0 < share * PER; i0 += UN * C::THREADS) {
+  for (int i0 = threadIdx.x; i0 < share << shift; i0 += UN * C::THREADS) {
     if (i0 != (int)threadIdx.x) load(i0);
 #pragma unroll
     for (int e = 0; e < UN; ++e) {
-      const int i = i0 + e * C::THREADS, r = tile_row(i / PER), q = i % PER;
+      const int i = i0 + e * C::THREADS, r = tile_row(i >> shift), q = i & (per - 1);
       const int s = r >> 7, rr = r & 127;
       const int tok = divide(rr, L.Gc, L.gc_inv), g = w.g0 + rr - tok * L.Gc;
-      if (i >= share * PER || g >= L.G) continue;
+      if (i >= share << shift || g >= L.G) continue;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int p = 0; p < P; ++p) {
-        const float f = wt[(i / PER) * P + p];
+        const float f = wt[(i >> shift) * P + p];
         o.x += f * v[e][p].x;
         o.y += f * v[e][p].y;
         o.z += f * v[e][p].z;
         o.w += f * v[e][p].w;
       }
       *reinterpret_cast<uint2*>(a.out + (int64_t)(w.q_row0 + w.tok0 + s * L.T + tok) * a.out_stride +
-                                (int64_t)(w.kvh * L.G + g) * DH + 4 * q) = make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
+                                (int64_t)(w.kvh * L.G + g) * DH + half * (DH / 2) + 4 * q) = make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
     }
   }
 }
@@ -371,7 +378,8 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
     tmem_alloc(&B->tmem, C::COLS);
     tmem_relinquish();
   }
-  const Unit w = find_unit<DH>(a, L, blockIdx.x / L.split);
+  const int half = (int)(blockIdx.x / L.split) & (L.vs - 1);
+  const Unit w = find_unit<DH>(a, L, (int)(blockIdx.x / L.split) >> (L.vs - 1));
   const uint8_t* mask = MASKED ? a.key_mask + w.kv_row0 : nullptr;
 
   // key tiles of every query tile: up to its last token's last key
@@ -446,10 +454,10 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
     const bool is_v = SB == 1 ? (i & 1) : (i > 0 && ((i & 1) == 0 || i + 1 == 2 * n_tiles));
     const int t = SB == 1 ? i >> 1 : (is_v ? (i + 1 == 2 * n_tiles ? n_tiles - 1 : (i >> 1) - 1) : (i + 1) >> 1);
     const int slot = loaded % NS;
-    mbar_arrive_expect_tx(&B->full[slot], C::SLOT);
+    mbar_arrive_expect_tx(&B->full[slot], is_v ? C::SLOT >> (L.vs - 1) : C::SLOT);
     tma_load_3d_nohint(smem + C::RING + slot * C::SLOT, is_v ? &vmap : &kmap, &B->full[slot], 0,
                        (int)(w.kv_row0 + (int64_t)(lo + tile_at(t)) * BK) + (is_v ? h * C::BKV : 0),
-                       w.kvh * DB + (is_v ? 0 : h * C::DBK));
+                       w.kvh * DB + (is_v ? half * (DB / 2) : h * C::DBK));
     ++loaded;
   };
   if (warp == C::W_LOAD && lane == 0 && n_tiles > 0) {
@@ -482,7 +490,8 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
     }
   } else if (warp == C::W_MMA) {
     // ---------------------------------------------------------------- MMAs
-    constexpr uint32_t idesc_s = idesc_bf16(128, BK), idesc_o = idesc_bf16(128, DH, true);
+    constexpr uint32_t idesc_s = idesc_bf16(128, BK);
+    const uint32_t idesc_o = C::VS && L.vs == 2 ? idesc_bf16(128, DH / 2, true) : idesc_bf16(128, DH, true);
     int c = 0;  // ring slots consumed
     bool ok = n_tiles == 0 || warp_wait(&B->q, 0, abort_flag, a.status);
     auto wait_slot = [&](int i) { return warp_wait(&B->full[i % NS], (uint32_t)(i / NS) & 1u, abort_flag, a.status); };
@@ -678,7 +687,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
         tc_fence_after();
         l *= factor;
 #pragma unroll 1
-        for (int d = 0; d < DH; d += 32) {
+        for (int d = 0; d < DH >> (L.vs - 1); d += 32) {
           uint32_t o[32];
           tmem_ld32_start(tm_o + d, o);
           tmem_ld_wait();
@@ -727,7 +736,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
       uint8_t* tile = smem + s * C::QBYTES;
       const bool whole = t0 + L.T <= w.n_new && w.g0 + L.Gc <= L.G;
 #pragma unroll 1
-      for (int d = 0; d < DB; ++d) {
+      for (int d = 0; d < DB >> (L.vs - 1); ++d) {
         uint32_t o[2][32];
         if (n > 0) {
           tmem_ld32_start(tm_o + 64 * d, o[0]);
@@ -751,7 +760,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
           if (s == 0) asm volatile("bar.sync 1, 128;" ::: "memory");
           else asm volatile("bar.sync 2, 128;" ::: "memory");
           if (row == 0 && ok) {
-            tma_store_3d(&omap, tile + d * (128 * 128), d * 64, w.kvh * L.G + w.g0, w.q_row0 + t0);
+            tma_store_3d(&omap, tile + d * (128 * 128), half * (DH / 2) + d * 64, w.kvh * L.G + w.g0, w.q_row0 + t0);
             bulk_commit();
           }
         }
@@ -762,12 +771,12 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
         __syncwarp();  // a warp stores the 32 rows it wrote
         constexpr int CPR = DH / 8, RPI = 32 / CPR;  // pieces of a row; rows an instruction
         const int r0 = 32 * (warp & 3) + lane / CPR, ch = lane % CPR;
-        bf16* out0 = a.out + (int64_t)(w.q_row0 + t0) * a.out_stride + (int64_t)(w.kvh * L.G + w.g0) * DH + 8 * ch;
+        bf16* out0 = a.out + (int64_t)(w.q_row0 + t0) * a.out_stride + (int64_t)(w.kvh * L.G + w.g0) * DH + half * (DH / 2) + 8 * ch;
         const int rows = min(32 * (warp & 3) + 32, min(L.T, w.n_new - t0) * L.Gc);
 #pragma unroll 8
         for (int r = r0; r < rows; r += RPI) {
           const int rt = divide(r, L.Gc, L.gc_inv), rg = r - rt * L.Gc;
-          if (w.g0 + rg < L.G)
+          if (w.g0 + rg < L.G && ch < CPR >> (L.vs - 1))
             *reinterpret_cast<uint4*>(out0 + rt * a.out_stride + rg * DH) =
                 *reinterpret_cast<const uint4*>(tile + (ch >> 3) * (128 * 128) + sw128_offset(r, ch & 7));
         }
@@ -779,7 +788,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
       reinterpret_cast<float2*>(smem + C::ML)[s * 128 + row] = ok ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
       uint8_t* part = smem + (s * 128 + row) * (DH * 4);
 #pragma unroll 1
-      for (int d = 0; d < DH; d += 32) {
+      for (int d = 0; d < DH >> (L.vs - 1); d += 32) {
         uint32_t o[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = 0u;
@@ -808,11 +817,12 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
     // the unit found again: kept in registers it would spill in the loops above
     unsigned bx = blockIdx.x;
     asm volatile("" : "+r"(bx));
-    const Unit w = find_unit<DH>(a, L, bx / L.split);
+    const int half = (int)(bx / L.split) & (L.vs - 1);
+    const Unit w = find_unit<DH>(a, L, (int)(bx / L.split) >> (L.vs - 1));
     const int rank = (int)cluster_rank();
-    if (L.split == 2) merge_rows<DH, 2>(a, L, w, smem, rank);
-    else if (L.split == 4) merge_rows<DH, 4>(a, L, w, smem, rank);
-    else merge_rows<DH, 8>(a, L, w, smem, rank);
+    if (L.split == 2) merge_rows<DH, 2>(a, L, w, smem, rank, half);
+    else if (L.split == 4) merge_rows<DH, 4>(a, L, w, smem, rank, half);
+    else merge_rows<DH, 8>(a, L, w, smem, rank, half);
     __syncthreads();
     cluster_arrive();  // no CTA leaves while a peer reads its partials
     cluster_wait();
@@ -858,23 +868,28 @@ cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
   // Split the keys of a unit over the CTAs of a cluster where that shortens the
   // launch: the longest unit, or the rounds of CTAs on an SM, whichever is more,
   // in clocks from measured costs of a key tile, of a unit's start and end, and of
-  // a merge.  (12.0 us against 14.6 unsplit for 16 rows over 1016 keys 32/8/128,
+  // a merge (less where SMs are left to halve the value dims).  (12.0 us against 14.6 unsplit for 16 rows over 1016 keys 32/8/128,
   // split by 4; 10.8 unsplit against 13.7 split by 2 for 400 tokens.)
   const double tile = DH == 64 ? 1500 : 2700, shared = 1800, ends = 8500;
   double best = 0;
-  L.split = 1;
+  L.split = L.vs = 1;
   for (int e = 0; e < 4; ++e) {
     const int n = 1 << e, ctas = g_resident[DH / 128][e] << e;  // at once
     if (ctas == 0 || longest < 2 * n - 1) continue;
-    const double step = (C::CTAS == 2 && n == 1 ? shared : tile), own = ends + (n > 1 ? 6000 + 10000.0 / n : 0);
+    const int vs = C::VS && units * n * 2 <= ctas ? 2 : 1;
+    const double step = (C::CTAS == 2 && n == 1 ? shared : tile);
+    const double own = (ends + (n > 1 ? 6000 + 10000.0 / n : 0)) * (vs == 2 ? 0.6 : 1);
     const double chain = own + tile * ((longest + n - 1) / n);
     const double all = (double)((units * n + ctas - 1) / ctas) * (own + step * steps / ((double)units * n));
     const double cost = chain > all ? chain : all;
     if (e == 0 || cost < best) {
       best = cost;
       L.split = n;
+      L.vs = vs;
     }
   }
+  // over the queries themselves the halves would not start with the same queries
+  if (a.out == a.q) L.vs = 1;
 
   CUtensorMap qmap, kmap, vmap, omap;
   cudaError_t e = make_bf16_3d_map(&qmap, a.q, {DH, a.Hq, a.cu_q[a.batch]}, {DH, (long)a.q_stride}, {64, L.Gc, L.T});
@@ -885,10 +900,10 @@ cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
                          {64, C::BK, C::DBK});
   if (e == cudaSuccess)
     e = make_bf16_3d_map(&vmap, a.v, {64, (long)a.cache_rows, (long)a.Hkv * C::DB}, {(long)a.kv_stride, 64},
-                         {64, C::BKV, C::DB});
+                         {64, C::BKV, C::DB / L.vs});
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * L.split));
+  cfg.gridDim = dim3((unsigned)(units * L.split * L.vs));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = L.split > 1 ? C::SPLIT_BYTES : C::BYTES;
   cfg.stream = st;

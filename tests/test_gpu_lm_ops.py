@@ -409,6 +409,27 @@ def test_attention_in_place_of_the_queries(experts, hq, hkv, dh):
     assert torch.equal(want, got) and torch.equal(token, over)
 
 
+@pytest.mark.parametrize("hq,hkv,dh", [(8, 1, 256), (3, 1, 256), (16, 2, 128), (5, 5, 128)])
+def test_prompt_attention_idle_sms(experts, hq, hkv, dh):
+    """Small calls, whose value dims two CTAs share, against the same calls over their queries, which
+    they do not share: whole and cut tiles, split keys, masks, wide output rows."""
+    import torch
+    ex, g = experts(hq, hkv, dh), generator(70)
+    for new, cached in (([16], [0]), ([5], [0]), ([1], [4000]), ([16], [1008]), ([130], [7]), ([33, 1], [90, 700])):
+        q, k, v, out = run_prompt(ex, hq, hkv, dh, new, cached, gap=2, seed=sum(new))
+        run_prompt(ex, hq, hkv, dh, new, cached, masked=0.4, gap=2, seed=1 + sum(new))
+        n = sum(new)
+        cu, lens = [0] + [int(x) for x in np.cumsum(new)], [a + b for a, b in zip(new, cached)]
+        row0 = [2 + sum(lens[:i]) + 2 * i for i in range(len(new))]
+        wide, view = strided(out[:n], 8)
+        wide.fill_(5.0)
+        ex.prompt_attention(q[:n], k, v, cu, row0, lens, out=view)
+        over = q[:n].clone()
+        ex.prompt_attention(over, k, v, cu, row0, lens, out=over)
+        ex.synchronize()
+        assert torch.equal(over, out[:n]) and torch.equal(view, out[:n]) and (wide[:, hq * dh:] == 5.0).all()
+
+
 # ---------------------------------------------------------------- token attention
 
 def run_token(ex, hq, hkv, dh, lens, max_len=None, masked=None, seed=0, room=7, scale=0.0):
