@@ -404,6 +404,17 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
     n_tiles = max(n_tiles, cnt[s]);
   }
 
+  const bool q_loaded = n_tiles > 0;
+  if (warp == C::W_LOAD && lane == 0 && q_loaded) {  // under the look at the mask
+    mbar_arrive_expect_tx(&B->q, (uint32_t)(NQ * DB * L.T * L.Gc * 128));
+#pragma unroll
+    for (int s = 0; s < NQ; ++s)
+#pragma unroll
+      for (int d = 0; d < DB; ++d)
+        tma_load_3d_nohint(smem + s * C::QBYTES + d * (128 * 128), &qmap, &B->q, d * 64, w.kvh * L.G + w.g0,
+                           w.q_row0 + w.tok0 + s * L.T);
+  }
+
   // Masked calls: the tiles that hold a valid key, in order, with the top bit
   // set when some of their keys are masked; all other tiles are skipped.  (Key
   // ranges beyond the list's room look every tile's mask up instead.)
@@ -461,13 +472,6 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
     ++loaded;
   };
   if (warp == C::W_LOAD && lane == 0 && n_tiles > 0) {
-    mbar_arrive_expect_tx(&B->q, (uint32_t)(NQ * DB * L.T * L.Gc * 128));
-#pragma unroll
-    for (int s = 0; s < NQ; ++s)
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-        tma_load_3d_nohint(smem + s * C::QBYTES + d * (128 * 128), &qmap, &B->q, d * 64, w.kvh * L.G + w.g0,
-                           w.q_row0 + w.tok0 + s * L.T);
     while (loaded < C::PARTS) load();  // the first tile's K; the rest after the CTA has met
   }
   tc_fence_before();
@@ -479,7 +483,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
     if (C::TRADE) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_AUX));
   if (warp == C::W_LOAD) {
     // ---------------------------------------------------------------- loads
-    if (lane == 0 && n_tiles > 0) {
+    if (lane == 0 && q_loaded) {
       while (loaded < 2 * C::PARTS * n_tiles &&
              (loaded < NS || mbar_wait(&B->empty[loaded % NS], (uint32_t)((loaded / NS) & 1) ^ 1u, abort_flag, a.status)))
         load();
