@@ -94,8 +94,8 @@ struct Cfg {
   static constexpr int WT = ML + NQ * 128 * 8;     // [rows of this CTA][split] weights of the merge
   static constexpr int LIST = BARS + 256;          // key tiles with valid keys (masked calls): entries, then states
   static constexpr int BYTES = LIST + kListTiles * 3 + 1024;
-  // a split launch asks for more than half an SM's: two CTAs of it would share
-  // SMs while others idle (16 tokens over 4080 keys 4/1/64)
+  // a split launch of no more CTAs than SMs asks for more than half an SM's: two
+  // CTAs of it would share SMs while others idle (16 tokens over 4080 keys 4/1/64)
   static constexpr int SPLIT_BYTES = BYTES > 120 * 1024 ? BYTES : 120 * 1024;
   // tensor memory columns: scores, then O
   static constexpr int O0 = NQ * SB * BK, COLS = O0 + NQ * DH <= 256 ? 256 : 512;
@@ -833,8 +833,8 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
   }
 }
 
-// Clusters of 1, 2, 4 and 8 CTAs that the GPU holds at once, for head_dim 64, 128,
-// 256 (the same for every GPU this library runs on).
+// Clusters of 1, 2, 4 and 8 CTAs with a SM each that the GPU holds at once, for
+// head_dim 64, 128, 256 (the same for every GPU this library runs on).
 int g_resident[3][4];
 
 template <int DH>
@@ -870,26 +870,37 @@ cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
   L.work_cu[n] = (int)units;
   L.per_inv = L.per > 1 && units * L.per < ((int64_t)1 << 32) ? (uint32_t)(((1ull << 32) + L.per - 1) / L.per) : 0;
   // Split the keys of a unit over the CTAs of a cluster where that shortens the
-  // launch: the longest unit, or the rounds of CTAs on an SM, whichever is more,
-  // in clocks from measured costs of a key tile, of a unit's start and end, and of
-  // a merge (less where SMs are left to halve the value dims).  (12.0 us against 14.6 unsplit for 16 rows over 1016 keys 32/8/128,
-  // split by 4; 10.8 unsplit against 13.7 split by 2 for 400 tokens.)
-  const double tile = DH == 64 ? 1500 : 2700, shared = 1800, ends = 8500;
+  // launch: the longest unit, or all units over the SMs, whichever is more, in
+  // clocks from measured costs of a key tile (alone; beside a second CTA of the
+  // SM), of a unit's start and end, and of a merge (less where SMs are left to
+  // halve the value dims).  At head_dim 64 the split CTAs have a SM each while
+  // there are as many, else two share one, and a half that is free is taken up at
+  // once; a SM of one CTA runs in rounds.  (12.0 us against 14.6 unsplit for 16
+  // rows over 1016 keys 32/8/128, split by 4; 10.8 unsplit against 13.7 split by 2
+  // for 400 tokens; 45 split by 2 against 54.5 for 8192 tokens 4/1/64, 101 unsplit
+  // against 128 for 12/4/64.)
+  const double tile = DH == 64 ? 1150 : 2700, shared = 1560, ends = 8500;
   double best = 0;
+  int smem = C::BYTES;
   L.split = L.vs = 1;
   for (int e = 0; e < 4; ++e) {
-    const int n = 1 << e, ctas = g_resident[DH / 128][e] << e;  // at once
-    if (ctas == 0 || longest < 2 * n - 1) continue;
+    const int n = 1 << e, clusters = g_resident[DH / 128][e];
+    if (clusters == 0 || longest < 2 * n - 1) continue;
+    const bool pairs = C::CTAS == 2 && (n == 1 || units > clusters);
+    const double ctas = (double)(clusters << e) * (pairs ? 2 : 1);  // at once
     const int vs = C::VS && units * n * 2 <= ctas ? 2 : 1;
-    const double step = (C::CTAS == 2 && n == 1 ? shared : tile);
-    const double own = (ends + (n > 1 ? 6000 + 10000.0 / n : 0)) * (vs == 2 ? 0.6 : 1);
+    const double merge = n == 1 ? 0 : (DH > 64 ? 6000 + 10000.0 / n : (pairs ? 4000 + 1000 * n : 6000));
+    const double own = (ends + merge) * (vs == 2 ? 0.6 : 1);
     const double chain = own + tile * ((longest + n - 1) / n);
-    const double all = (double)((units * n + ctas - 1) / ctas) * (own + step * steps / ((double)units * n));
+    double rounds = (double)units * n / ctas;
+    rounds = !pairs ? ceil(rounds) : (rounds > 1 ? rounds + 0.35 : rounds);  // 0.35: the last ones' overhang
+    const double all = rounds * (own + (pairs ? shared : tile) * steps / ((double)units * n));
     const double cost = chain > all ? chain : all;
     if (e == 0 || cost < best) {
       best = cost;
       L.split = n;
       L.vs = vs;
+      smem = n > 1 && !pairs ? C::SPLIT_BYTES : C::BYTES;
     }
   }
   // over the queries themselves the halves would not start with the same queries
@@ -909,7 +920,7 @@ cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(units * L.split * L.vs));
   cfg.blockDim = dim3(C::THREADS);
-  cfg.dynamicSmemBytes = L.split > 1 ? C::SPLIT_BYTES : C::BYTES;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -939,7 +950,7 @@ static cudaError_t setup() {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(8);
     cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = i > 0 ? C::SPLIT_BYTES : C::BYTES;
+    cfg.dynamicSmemBytes = C::SPLIT_BYTES;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 1u << i;

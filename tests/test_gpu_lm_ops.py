@@ -409,6 +409,17 @@ def test_attention_in_place_of_the_queries(experts, hq, hkv, dh):
     assert torch.equal(want, got) and torch.equal(token, over)
 
 
+@pytest.mark.parametrize("hq,hkv,dh,new,cached", [
+    (4, 1, 64, [2048], [0]), (4, 1, 64, [100] * 8 + [2100], [0] * 9), (2, 1, 64, [900, 2500, 1], [0, 300, 2000]),
+    (6, 6, 64, [64] * 4, [1500, 1700, 900, 1601])])
+def test_prompt_attention_two_split_ctas_a_sm(experts, hq, hkv, dh, new, cached):
+    """Split key ranges of more CTAs than SMs, whole and masked, causal and not."""
+    ex = experts(hq, hkv, dh)
+    run_prompt(ex, hq, hkv, dh, new, cached, gap=1, seed=80)
+    run_prompt(ex, hq, hkv, dh, new, cached, gap=1, seed=81, causal=False, masked=0.5)
+    run_prompt(ex, hq, hkv, dh, new, cached, gap=1, seed=82, masked=lambda i, m: i // 200 % 2 == 1)
+
+
 @pytest.mark.parametrize("hq,hkv,dh", [(8, 1, 256), (3, 1, 256), (16, 2, 128), (5, 5, 128)])
 def test_prompt_attention_idle_sms(experts, hq, hkv, dh):
     """Small calls, whose value dims two CTAs share, against the same calls over their queries, which
