@@ -19,6 +19,9 @@
 //     the MMAs 2048.  32768 tokens 32/8/128: 4.8 ms, 1830 TFLOP/s; bound by the
 //     MMA rate, shared memory's bandwidth near it (operands and TMA writes take
 //     2048 clocks a step too).
+//     Where SMs would idle, one tile a CTA with two S buffers, as at 256: a key
+//     tile then takes 1450 clocks (16/2/128: 1500 tokens 14.7 us against 22.3 with
+//     two tiles a CTA, 4096 48.3 against 55.2 with one).
 //   head_dim 256: O fills half of tensor memory; one tile, two S buffers, the
 //     next Q K^T under this softmax; K and V in half tiles so that a ring of five
 //     fits beside Q.  8192 tokens 8/1/256: 150 us, 1830 TFLOP/s.  (Key tiles of
@@ -64,9 +67,9 @@ using namespace tc;
 constexpr int kListTiles = 512;
 constexpr float kRaise = 8.f;  // log2: raise the exponent reference past this
 
-template <int DH>
+template <int DH, int NQ_>
 struct Cfg {
-  static constexpr int NQ = DH == 128 ? 2 : 1;     // query tiles of a CTA
+  static constexpr int NQ = NQ_;                   // query tiles of a CTA
   static constexpr int SB = NQ == 1 ? 2 : 1;     // score buffers of a query tile
   static constexpr int CTAS = DH == 64 ? 2 : 1;    // resident a SM
   static constexpr int BK = DH == 64 ? 96 : 128;                   // keys of a tile
@@ -244,7 +247,7 @@ __device__ __forceinline__ int divide(int x, int d, uint32_t inv) {
   return d == 1 ? x : (inv != 0u ? (int)__umulhi((uint32_t)x, inv) : x / d);
 }
 
-template <int DH>
+template <int NQ>
 __device__ __forceinline__ Unit find_unit(const PromptAttnArgs& a, const Launch& L, int u) {
   int i = 0;
   if (L.n_order > 1) {
@@ -263,7 +266,7 @@ __device__ __forceinline__ Unit find_unit(const PromptAttnArgs& a, const Launch&
   const int t = divide(u, L.per, L.per_inv), h = u - t * L.per;
   w.kvh = L.hc == 1 ? h : h / L.hc;
   w.g0 = (h - w.kvh * L.hc) * L.Gc;
-  w.tok0 = t * L.T * Cfg<DH>::NQ;
+  w.tok0 = t * L.T * NQ;
   return w;
 }
 
@@ -272,10 +275,10 @@ __device__ __forceinline__ Unit find_unit(const PromptAttnArgs& a, const Launch&
 // weights 2^(m_p - m) / l of every split.  Bound by remote shared memory (15 bytes
 // a clock measured with all of them in flight), so rows that hold no query are
 // left out: 16 tokens over 1016 keys 32/8/128 9.8 us, 12.4 with them.
-template <int DH, int P>
+template <int DH, int NQ, int P>
 __device__ __forceinline__ void merge_rows(const PromptAttnArgs& a, const Launch& L, const Unit& w, uint8_t* smem,
                                            int rank, int half) {
-  using C = Cfg<DH>;
+  using C = Cfg<DH, NQ>;
   constexpr int UN = 16 / P;
   const int shift = C::LOG_DIMS - 1 - L.vs, per = 1 << shift;  // pieces of a row
   const int rows0 = max(0, min(L.T, w.n_new - w.tok0)) * L.Gc;
@@ -340,14 +343,14 @@ __device__ __forceinline__ void merge_rows(const PromptAttnArgs& a, const Launch
 }
 
 // MASKED: the call has a key mask.
-template <int DH, bool MASKED>
-__global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
+template <int DH, int NQ, bool MASKED>
+__global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, Cfg<DH, NQ>::CTAS)
     k_prompt_attn(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap,
                   const __grid_constant__ PromptAttnArgs a,
                   const __grid_constant__ Launch L) {
-  using C = Cfg<DH>;
-  constexpr int NQ = C::NQ, SB = C::SB, BK = C::BK, DB = C::DB, NS = C::NS;
+  using C = Cfg<DH, NQ>;
+  constexpr int SB = C::SB, BK = C::BK, DB = C::DB, NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   Bars* B = reinterpret_cast<Bars*>(smem + C::BARS);
@@ -379,7 +382,7 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
     tmem_relinquish();
   }
   const int half = (int)(blockIdx.x / L.split) & (L.vs - 1);
-  const Unit w = find_unit<DH>(a, L, (int)(blockIdx.x / L.split) >> (L.vs - 1));
+  const Unit w = find_unit<NQ>(a, L, (int)(blockIdx.x / L.split) >> (L.vs - 1));
   const uint8_t* mask = MASKED ? a.key_mask + w.kv_row0 : nullptr;
 
   // key tiles of every query tile: up to its last token's last key
@@ -822,11 +825,11 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
     unsigned bx = blockIdx.x;
     asm volatile("" : "+r"(bx));
     const int half = (int)(bx / L.split) & (L.vs - 1);
-    const Unit w = find_unit<DH>(a, L, (int)(bx / L.split) >> (L.vs - 1));
+    const Unit w = find_unit<NQ>(a, L, (int)(bx / L.split) >> (L.vs - 1));
     const int rank = (int)cluster_rank();
-    if (L.split == 2) merge_rows<DH, 2>(a, L, w, smem, rank, half);
-    else if (L.split == 4) merge_rows<DH, 4>(a, L, w, smem, rank, half);
-    else merge_rows<DH, 8>(a, L, w, smem, rank, half);
+    if (L.split == 2) merge_rows<DH, NQ, 2>(a, L, w, smem, rank, half);
+    else if (L.split == 4) merge_rows<DH, NQ, 4>(a, L, w, smem, rank, half);
+    else merge_rows<DH, NQ, 8>(a, L, w, smem, rank, half);
     __syncthreads();
     cluster_arrive();  // no CTA leaves while a peer reads its partials
     cluster_wait();
@@ -837,10 +840,11 @@ __global__ void __launch_bounds__(Cfg<DH>::THREADS, Cfg<DH>::CTAS)
 // head_dim 64, 128, 256 (the same for every GPU this library runs on).
 int g_resident[3][4];
 
-template <int DH>
-cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
-  using C = Cfg<DH>;
-  Launch L;
+// The units of a call and their split; its cost in clocks, negative when there are
+// too many units.
+template <int DH, int NQ>
+double plan(const PromptAttnArgs& a, Launch& L, int& smem, int64_t& units) {
+  using C = Cfg<DH, NQ>;
   L.G = a.Hq / a.Hkv;
   L.hc = (L.G + 127) / 128;
   L.Gc = (L.G + L.hc - 1) / L.hc;
@@ -856,7 +860,7 @@ cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
       L.order[i] = (uint8_t)b;
     }
   L.n_order = n;
-  int64_t units = 0;
+  units = 0;
   double steps = 0;  // key tiles of all units
   const int longest = (a.kv_len[L.order[0]] + C::BK - 1) / C::BK;  // of one unit
   for (int i = 0; i < n; ++i) {
@@ -865,7 +869,7 @@ cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
     const int64_t mine = (int64_t)((tok + L.T * C::NQ - 1) / (L.T * C::NQ)) * a.Hkv * L.hc;
     steps += (double)mine * (a.causal ? a.kv_len[b] - 0.5 * tok : a.kv_len[b]) / C::BK + 0.5 * mine;
     units += mine;
-    if (units > 0x7fffffff / 8) return cudaErrorInvalidConfiguration;
+    if (units > 0x7fffffff / 8) return -1;
   }
   L.work_cu[n] = (int)units;
   L.per_inv = L.per > 1 && units * L.per < ((int64_t)1 << 32) ? (uint32_t)(((1ull << 32) + L.per - 1) / L.per) : 0;
@@ -873,15 +877,16 @@ cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
   // launch: the longest unit, or all units over the SMs, whichever is more, in
   // clocks from measured costs of a key tile (alone; beside a second CTA of the
   // SM), of a unit's start and end, and of a merge (less where SMs are left to
-  // halve the value dims).  At head_dim 64 the split CTAs have a SM each while
-  // there are as many, else two share one, and a half that is free is taken up at
-  // once; a SM of one CTA runs in rounds.  (12.0 us against 14.6 unsplit for 16
-  // rows over 1016 keys 32/8/128, split by 4; 10.8 unsplit against 13.7 split by 2
-  // for 400 tokens; 45 split by 2 against 54.5 for 8192 tokens 4/1/64, 101 unsplit
-  // against 128 for 12/4/64.)
-  const double tile = DH == 64 ? 1150 : 2700, shared = 1560, ends = 8500;
+  // halve the value dims).  Equal units run in whole rounds, those of a causal
+  // prompt, longest first, fill the SMs but for an overhang.  At head_dim 64 the
+  // split CTAs have a SM each while there are as many, else two share one.
+  // Measured, chosen against other: 16 rows over 1016 keys 32/8/128 8.4 split by
+  // 4, 14.6 unsplit; 400 tokens 10.8 unsplit, 13.7 split by 2; 8192 tokens 4/1/64
+  // 45 split by 2, 54.5 unsplit, 12/4/64 101 unsplit, 128 split by 2.
+  const double tile = DH == 64 ? 1150 : (DH == 128 && NQ == 1 ? 1450 : 2700), shared = 1560;
+  const double ends = DH == 128 && NQ == 1 ? 7000 : 8500, overhang = 0.35;
   double best = 0;
-  int smem = C::BYTES;
+  smem = C::BYTES;
   L.split = L.vs = 1;
   for (int e = 0; e < 4; ++e) {
     const int n = 1 << e, clusters = g_resident[DH / 128][e];
@@ -889,12 +894,18 @@ cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
     const bool pairs = C::CTAS == 2 && (n == 1 || units > clusters);
     const double ctas = (double)(clusters << e) * (pairs ? 2 : 1);  // at once
     const int vs = C::VS && units * n * 2 <= ctas ? 2 : 1;
-    const double merge = n == 1 ? 0 : (DH > 64 ? 6000 + 10000.0 / n : (pairs ? 4000 + 1000 * n : 6000));
+    const double merge = n == 1 ? 0 : (DH > 64 ? 3000 + (3000 + 10000.0 / n) * (NQ * DH / 256.0) : (pairs ? 4000 + 1000 * n : 6000));
     const double own = (ends + merge) * (vs == 2 ? 0.6 : 1);
     const double chain = own + tile * ((longest + n - 1) / n);
+    const double mean = own + (pairs ? shared : tile) * steps / ((double)units * n);
     double rounds = (double)units * n / ctas;
-    rounds = !pairs ? ceil(rounds) : (rounds > 1 ? rounds + 0.35 : rounds);  // 0.35: the last ones' overhang
-    const double all = rounds * (own + (pairs ? shared : tile) * steps / ((double)units * n));
+    if (!pairs) {
+      const double even = fmax(0.0, fmin(1.0, 2 * mean / chain - 1));  // 1: equal units
+      rounds = even * ceil(rounds) + (1 - even) * fmin(ceil(rounds), rounds + overhang);
+    } else if (rounds > 1) {
+      rounds += overhang;
+    }
+    const double all = rounds * mean;
     const double cost = chain > all ? chain : all;
     if (e == 0 || cost < best) {
       best = cost;
@@ -905,7 +916,12 @@ cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
   }
   // over the queries themselves the halves would not start with the same queries
   if (a.out == a.q) L.vs = 1;
+  return best;
+}
 
+template <int DH, int NQ>
+cudaError_t run(const PromptAttnArgs& a, const Launch& L, int smem, int64_t units, cudaStream_t st) {
+  using C = Cfg<DH, NQ>;
   CUtensorMap qmap, kmap, vmap, omap;
   cudaError_t e = make_bf16_3d_map(&qmap, a.q, {DH, a.Hq, a.cu_q[a.batch]}, {DH, (long)a.q_stride}, {64, L.Gc, L.T});
   if (e == cudaSuccess)
@@ -928,8 +944,26 @@ cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = L.split > 1 ? 1 : 0;
-  return a.key_mask ? cudaLaunchKernelEx(&cfg, k_prompt_attn<DH, true>, qmap, kmap, vmap, omap, a, L)
-                    : cudaLaunchKernelEx(&cfg, k_prompt_attn<DH, false>, qmap, kmap, vmap, omap, a, L);
+  return a.key_mask ? cudaLaunchKernelEx(&cfg, k_prompt_attn<DH, NQ, true>, qmap, kmap, vmap, omap, a, L)
+                    : cudaLaunchKernelEx(&cfg, k_prompt_attn<DH, NQ, false>, qmap, kmap, vmap, omap, a, L);
+}
+
+template <int DH>
+cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
+  constexpr int NQ = DH == 128 ? 2 : 1;
+  Launch L;
+  int smem;
+  int64_t units;
+  const double cost = plan<DH, NQ>(a, L, smem, units);
+  if (cost < 0) return cudaErrorInvalidConfiguration;
+  if (NQ == 2 && units <= 2 * g_resident[DH / 128][0]) {  // single tiles may fill the SMs better
+    Launch L1;
+    int smem1;
+    int64_t units1;
+    const double cost1 = plan<DH, 1>(a, L1, smem1, units1);
+    if (cost1 >= 0 && cost1 < cost) return run<DH, 1>(a, L1, smem1, units1, st);
+  }
+  return run<DH, NQ>(a, L, smem, units, st);
 }
 
 }  // namespace
@@ -940,11 +974,11 @@ cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int dh, cudaStream_
   return launch<256>(a, s);
 }
 
-template <int DH>
+template <int DH, int NQ>
 static cudaError_t setup() {
-  using C = Cfg<DH>;
+  using C = Cfg<DH, NQ>;
   cudaError_t e = cudaSuccess;
-  for (auto kern : {k_prompt_attn<DH, false>, k_prompt_attn<DH, true>})
+  for (auto kern : {k_prompt_attn<DH, NQ, false>, k_prompt_attn<DH, NQ, true>})
     if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SPLIT_BYTES);
   for (int i = 0; i < 4 && e == cudaSuccess; ++i) {
     cudaLaunchConfig_t cfg = {};
@@ -957,15 +991,16 @@ static cudaError_t setup() {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&g_resident[DH / 128][i], k_prompt_attn<DH, false>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&g_resident[DH / 128][i], k_prompt_attn<DH, NQ, false>, &cfg);
   }
   return e;
 }
 
 cudaError_t prompt_kernel_setup() {
-  cudaError_t e = setup<64>();
-  if (e == cudaSuccess) e = setup<128>();
-  if (e == cudaSuccess) e = setup<256>();
+  cudaError_t e = setup<64, 1>();
+  if (e == cudaSuccess) e = setup<128, 1>();
+  if (e == cudaSuccess) e = setup<128, 2>();
+  if (e == cudaSuccess) e = setup<256, 1>();
   return e;
 }
 

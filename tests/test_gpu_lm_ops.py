@@ -409,6 +409,17 @@ def test_attention_in_place_of_the_queries(experts, hq, hkv, dh):
     assert torch.equal(want, got) and torch.equal(token, over)
 
 
+@pytest.mark.parametrize("new,cached", [
+    ([1200, 63, 65, 1, 900, 257], [0, 0, 5, 300, 0, 1]), ([100, 64, 128, 33, 65, 129, 1, 32] * 2, [0] * 16),
+    ([64, 60, 64], [3936, 4000, 3900])])
+def test_prompt_attention_two_tiles_a_cta(experts, new, cached):
+    """Calls at head_dim 128 that fill the SMs with pairs of query tiles (the last: with split keys)."""
+    ex = experts(32, 8, 128)
+    run_prompt(ex, 32, 8, 128, new, cached, gap=1, seed=90)
+    run_prompt(ex, 32, 8, 128, new, cached, gap=1, seed=91, causal=False, masked=0.5)
+    run_prompt(ex, 32, 8, 128, new, cached, gap=1, seed=92, masked=lambda i, m: i // 150 % 2 == 1)
+
+
 @pytest.mark.parametrize("hq,hkv,dh,new,cached", [
     (4, 1, 64, [2048], [0]), (4, 1, 64, [100] * 8 + [2100], [0] * 9), (2, 1, 64, [900, 2500, 1], [0, 300, 2000]),
     (6, 6, 64, [64] * 4, [1500, 1700, 900, 1601])])
