@@ -733,6 +733,9 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, Cfg<DH, NQ>::CTAS)
     if (ok && n > 0)
       ok = SB == 2 ? warp_wait(&B->o[(n - 1) & 1], (uint32_t)((n - 1) >> 1) & 1u, abort_flag, a.status)
                    : warp_wait(&B->o[s], 0, abort_flag, a.status);
+    // a masked tile without keys has waited for nothing yet, and its zeros go over
+    // the query tile: the queries must have landed
+    if (MASKED && n == 0 && q_loaded) ok = warp_wait(&B->q, 0, abort_flag, a.status);
     __syncwarp();
     tc_fence_after();
     if (L.split == 1) {

@@ -328,6 +328,37 @@ def test_prompt_attention_key_tile_ends(experts, hq, hkv, dh, keys):
         run_prompt(ex, hq, hkv, dh, [4, 30], [keys - 4, keys - 30], masked=cut, gap=1, seed=keys + 2)
 
 
+@pytest.mark.parametrize("hq,hkv,dh,new,cached", [
+    (8, 1, 256, [700], [0]), (32, 8, 128, [700, 300], [0, 0]), (32, 8, 128, [64], [1000]), (12, 4, 64, [700], [0]),
+    (32, 8, 128, [64] * 40, [0] * 40), (4, 1, 64, [10], [4000])])
+def test_prompt_attention_rows_without_keys_are_zero_every_time(experts, hq, hkv, dh, new, cached):
+    """Query tiles all of whose keys are masked write their zeros where the queries land: many calls,
+    the copies cold and warm, all the same bits."""
+    import torch
+    ex, g = experts(hq, hkv, dh), generator(61)
+    cu, lens = [0] + [int(x) for x in np.cumsum(new)], [a + b for a, b in zip(new, cached)]
+    row0 = [0] + [int(x) for x in np.cumsum(lens)[:-1]]
+    rows = sum(lens)
+    q, k, v = normal(g, cu[-1], hq * dh), normal(g, rows, hkv * dh), normal(g, rows, hkv * dh)
+    mask = torch.zeros(rows, dtype=torch.uint8, device="cuda")
+    for r0, m in zip(row0, lens):
+        mask[r0 + m // 2:r0 + m] = 1  # a sequence's first half is masked
+    if len(new) > 2 or cached[0] > 3000:
+        mask[:] = 0
+    ref, mag = lm_ops.packed_attention(f64(q), f64(k), f64(v), hq, hkv, cu, row0, lens, mask.cpu().numpy())
+    want = ex.prompt_attention(q, k, v, cu, row0, lens, key_mask=mask)
+    ex.synchronize()
+    check_attention(f64(want), ref, mag)
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    outs = []
+    for i in range(60):
+        if i % 3 == 0:
+            flush.fill_(i)
+        outs.append(ex.prompt_attention(q, k, v, cu, row0, lens, key_mask=mask, out=torch.full_like(q, 3.0)))
+    ex.synchronize()
+    assert all(torch.equal(want, o) for o in outs)
+
+
 @pytest.mark.parametrize("std,scale", [(30.0, 0.0), (1.0, 3.0), (1e-3, 0.0), (1.0, 1e-4)])
 def test_prompt_attention_score_ranges(experts, std, scale):
     """Peaked and flat softmaxes (scores of several hundred, scores near zero)."""
