@@ -412,7 +412,7 @@ def test_prompt_attention_most_sequences(experts):
     check_attention(f64(out), ref, mag)
 
 
-@pytest.mark.parametrize("hq,hkv,dh", [(130, 1, 64), (262, 2, 64), (200, 1, 64), (66, 2, 128)])
+@pytest.mark.parametrize("hq,hkv,dh", [(130, 1, 64), (262, 2, 64), (200, 1, 64), (66, 2, 128), (130, 1, 128), (33, 1, 256)])
 def test_prompt_attention_wide_groups(hq, hkv, dh):
     """Groups of more heads than a query tile has rows, and just above half of them."""
     ex = _expert(hq, hkv, dh)
