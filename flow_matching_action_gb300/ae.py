@@ -371,6 +371,8 @@ class ActionExpert:
     """Convenience owner of one context: create / bind / sample / destroy.
 
     Holds references to the borrowed prefix tensors so they outlive the binding.
+    Calls enqueue on the context's stream: tensors (returned ones too) have to be
+    ready and used there, or ordered with it, and stay allocated until it is done.
     """
 
     def __init__(self, dims, weights: Dict, max_batch: int, max_prefix_rows: int, stream=None,
