@@ -54,6 +54,8 @@
 // still idle take half of the value dims each (the scores twice, the rest once):
 // the P V, the output and the merge of a CTA are halved.  16 tokens over 4080 keys
 // 8/1/256: 12.3 us against 15.2 with whole rows; a prompt of 50: 7.3 against 7.5.
+// (Not for pairs of tiles, which single ones replace before SMs idle: 8 prompts of
+// 64 tokens 32/8/128 6.0 us in single tiles, 6.4 in pairs with halved dims.)
 #include <math.h>
 
 #include "ae_internal.h"
@@ -86,7 +88,7 @@ struct Cfg {
   // MMAs).  It hands registers to the others where the launch's would not do:
   // 104 + 2 * 200 = 3 * 168 (NQ = 2), 96 + 160 = 2 * 128 (two CTAs a SM).
   static constexpr int THREADS = NQ * 128 + 128;
-  static constexpr bool VS = DH > 64;              // the value dims may be halved
+  static constexpr bool VS = DH > 64 && NQ == 1;   // the value dims may be halved
   static constexpr bool TRADE = NQ == 2 || CTAS == 2;
   static constexpr int REGS_AUX = NQ == 2 ? 104 : 96, REGS_MAX = NQ == 2 ? 200 : 160;
   static constexpr int W_LOAD = NQ * 4, W_MMA = NQ * 4 + 1;
@@ -280,7 +282,8 @@ __device__ __forceinline__ void merge_rows(const PromptAttnArgs& a, const Launch
                                            int rank, int half) {
   using C = Cfg<DH, NQ>;
   constexpr int UN = 16 / P;
-  const int shift = C::LOG_DIMS - 1 - L.vs, per = 1 << shift;  // pieces of a row
+  const int vs = C::VS ? L.vs : 1;
+  const int shift = C::LOG_DIMS - 1 - vs, per = 1 << shift;  // pieces of a row
   const int rows0 = max(0, min(L.T, w.n_new - w.tok0)) * L.Gc;
   const int rows = rows0 + (C::NQ == 2 ? max(0, min(L.T, w.n_new - w.tok0 - L.T)) * L.Gc : 0);
   const int i_lo = rows * rank / P, share = rows * (rank + 1) / P - i_lo;
@@ -350,6 +353,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, Cfg<DH, NQ>::CTAS)
                   const __grid_constant__ PromptAttnArgs a,
                   const __grid_constant__ Launch L) {
   using C = Cfg<DH, NQ>;
+  const int vs = C::VS ? L.vs : 1;
   constexpr int SB = C::SB, BK = C::BK, DB = C::DB, NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -381,8 +385,8 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, Cfg<DH, NQ>::CTAS)
     tmem_alloc(&B->tmem, C::COLS);
     tmem_relinquish();
   }
-  const int half = (int)(blockIdx.x / L.split) & (L.vs - 1);
-  const Unit w = find_unit<NQ>(a, L, (int)(blockIdx.x / L.split) >> (L.vs - 1));
+  const int half = (int)(blockIdx.x / L.split) & (vs - 1);
+  const Unit w = find_unit<NQ>(a, L, (int)(blockIdx.x / L.split) >> (vs - 1));
   const uint8_t* mask = MASKED ? a.key_mask + w.kv_row0 : nullptr;
 
   // key tiles of every query tile: up to its last token's last key
@@ -468,7 +472,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, Cfg<DH, NQ>::CTAS)
     const bool is_v = SB == 1 ? (i & 1) : (i > 0 && ((i & 1) == 0 || i + 1 == 2 * n_tiles));
     const int t = SB == 1 ? i >> 1 : (is_v ? (i + 1 == 2 * n_tiles ? n_tiles - 1 : (i >> 1) - 1) : (i + 1) >> 1);
     const int slot = loaded % NS;
-    mbar_arrive_expect_tx(&B->full[slot], is_v ? C::SLOT >> (L.vs - 1) : C::SLOT);
+    mbar_arrive_expect_tx(&B->full[slot], is_v ? C::SLOT >> (vs - 1) : C::SLOT);
     tma_load_3d_nohint(smem + C::RING + slot * C::SLOT, is_v ? &vmap : &kmap, &B->full[slot], 0,
                        (int)(w.kv_row0 + (int64_t)(lo + tile_at(t)) * BK) + (is_v ? h * C::BKV : 0),
                        w.kvh * DB + (is_v ? half * (DB / 2) : h * C::DBK));
@@ -498,7 +502,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, Cfg<DH, NQ>::CTAS)
   } else if (warp == C::W_MMA) {
     // ---------------------------------------------------------------- MMAs
     constexpr uint32_t idesc_s = idesc_bf16(128, BK);
-    const uint32_t idesc_o = C::VS && L.vs == 2 ? idesc_bf16(128, DH / 2, true) : idesc_bf16(128, DH, true);
+    const uint32_t idesc_o = vs == 2 ? idesc_bf16(128, DH / 2, true) : idesc_bf16(128, DH, true);
     int c = 0;  // ring slots consumed
     bool ok = n_tiles == 0 || warp_wait(&B->q, 0, abort_flag, a.status);
     auto wait_slot = [&](int i) { return warp_wait(&B->full[i % NS], (uint32_t)(i / NS) & 1u, abort_flag, a.status); };
@@ -694,7 +698,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, Cfg<DH, NQ>::CTAS)
         tc_fence_after();
         l *= factor;
 #pragma unroll 1
-        for (int d = 0; d < DH >> (L.vs - 1); d += 32) {
+        for (int d = 0; d < DH >> (vs - 1); d += 32) {
           uint32_t o[32];
           tmem_ld32_start(tm_o + d, o);
           tmem_ld_wait();
@@ -746,7 +750,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, Cfg<DH, NQ>::CTAS)
       uint8_t* tile = smem + s * C::QBYTES;
       const bool whole = t0 + L.T <= w.n_new && w.g0 + L.Gc <= L.G;
 #pragma unroll 1
-      for (int d = 0; d < DB >> (L.vs - 1); ++d) {
+      for (int d = 0; d < DB >> (vs - 1); ++d) {
         uint32_t o[2][32];
         if (n > 0) {
           tmem_ld32_start(tm_o + 64 * d, o[0]);
@@ -786,7 +790,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, Cfg<DH, NQ>::CTAS)
 #pragma unroll 8
         for (int r = r0; r < rows; r += RPI) {
           const int rt = divide(r, L.Gc, L.gc_inv), rg = r - rt * L.Gc;
-          if (w.g0 + rg < L.G && ch < CPR >> (L.vs - 1))
+          if (w.g0 + rg < L.G && ch < CPR >> (vs - 1))
             *reinterpret_cast<uint4*>(out0 + rt * a.out_stride + rg * DH) =
                 *reinterpret_cast<const uint4*>(tile + (ch >> 3) * (128 * 128) + sw128_offset(r, ch & 7));
         }
@@ -798,7 +802,7 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, Cfg<DH, NQ>::CTAS)
       reinterpret_cast<float2*>(smem + C::ML)[s * 128 + row] = ok ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
       uint8_t* part = smem + (s * 128 + row) * (DH * 4);
 #pragma unroll 1
-      for (int d = 0; d < DH >> (L.vs - 1); d += 32) {
+      for (int d = 0; d < DH >> (vs - 1); d += 32) {
         uint32_t o[32];
 #pragma unroll
         for (int j = 0; j < 32; ++j) o[j] = 0u;
@@ -827,8 +831,8 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, Cfg<DH, NQ>::CTAS)
     // the unit found again: kept in registers it would spill in the loops above
     unsigned bx = blockIdx.x;
     asm volatile("" : "+r"(bx));
-    const int half = (int)(bx / L.split) & (L.vs - 1);
-    const Unit w = find_unit<NQ>(a, L, (int)(bx / L.split) >> (L.vs - 1));
+    const int half = (int)(bx / L.split) & (vs - 1);
+    const Unit w = find_unit<NQ>(a, L, (int)(bx / L.split) >> (vs - 1));
     const int rank = (int)cluster_rank();
     if (L.split == 2) merge_rows<DH, NQ, 2>(a, L, w, smem, rank, half);
     else if (L.split == 4) merge_rows<DH, NQ, 4>(a, L, w, smem, rank, half);

@@ -442,13 +442,20 @@ def test_attention_in_place_of_the_queries(experts, hq, hkv, dh):
 
 @pytest.mark.parametrize("new,cached", [
     ([1200, 63, 65, 1, 900, 257], [0, 0, 5, 300, 0, 1]), ([100, 64, 128, 33, 65, 129, 1, 32] * 2, [0] * 16),
-    ([64, 60, 64], [3936, 4000, 3900])])
+    ([64, 60, 64], [3936, 4000, 3900]), ([64, 50, 33, 64, 64, 64, 64, 61], [0] * 8), ([128] * 4, [0] * 4)])
 def test_prompt_attention_two_tiles_a_cta(experts, new, cached):
-    """Calls at head_dim 128 that fill the SMs with pairs of query tiles (the last: with split keys)."""
+    """Calls at head_dim 128 that fill the SMs with pairs of query tiles, and one that does not."""
     ex = experts(32, 8, 128)
     run_prompt(ex, 32, 8, 128, new, cached, gap=1, seed=90)
     run_prompt(ex, 32, 8, 128, new, cached, gap=1, seed=91, causal=False, masked=0.5)
     run_prompt(ex, 32, 8, 128, new, cached, gap=1, seed=92, masked=lambda i, m: i // 150 % 2 == 1)
+
+
+def test_prompt_attention_two_tiles_over_split_keys(experts):
+    """Pairs of query tiles whose long key ranges are split over eight CTAs."""
+    ex = experts(5, 5, 128)
+    run_prompt(ex, 5, 5, 128, [520], [59480], gap=1, seed=95)
+    run_prompt(ex, 5, 5, 128, [520], [59480], gap=1, seed=96, masked=0.5)
 
 
 @pytest.mark.parametrize("hq,hkv,dh,new,cached", [
