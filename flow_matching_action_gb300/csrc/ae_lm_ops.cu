@@ -136,7 +136,8 @@ ae_status ae_qk_norm_rope(ae_ctx* c, const ae_qk_norm_rope_args* p) {
   AE_TRY(check_rows(c, "q_out", p->q_out, p->q_stride, d.qdim()));
   AE_TRY(check_rows(c, "k_cache", p->k_cache, p->kv_stride, d.kvdim()));
   AE_TRY(check_rows(c, "v_cache", p->v_cache, p->kv_stride, d.kvdim()));
-  if (p->q_out == p->qkv && p->q_stride != p->qkv_stride)
+  // in place, a row must land on itself (one row does, whatever its strides are)
+  if (p->q_out == p->qkv && p->tokens > 1 && p->q_stride != p->qkv_stride)
     return fail(c, AE_ERR_INVALID_ARG, "q_out is qkv but the row strides differ");
   for (const void* w : {p->q_norm, p->k_norm})
     if ((uintptr_t)w % 16 != 0) return fail(c, AE_ERR_INVALID_ARG, "a norm weight is not 16-byte aligned");

@@ -307,7 +307,8 @@ typedef struct {
                                 K and V are not stored; >= cache_rows: not stored, and the context's status
                                 becomes AE_ERR_DEVICE.  NULL: token t goes to row t */
   int64_t cache_rows;        /* rows of k_cache / v_cache (>= tokens without kv_rows) */
-  void* q_out;               /* device bf16 [tokens][Hq dh]; may be qkv with q_stride == qkv_stride (in place) */
+  void* q_out;               /* device bf16 [tokens][Hq dh]; may be qkv with q_stride == qkv_stride (in place;
+                                one token: any strides) */
   int64_t q_stride;
   void *k_cache, *v_cache;   /* device bf16 [cache_rows][Hkv dh], no overlap with qkv or q_out */
   int64_t kv_stride;
