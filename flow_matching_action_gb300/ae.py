@@ -9,6 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import sys
 from typing import Dict, Optional, Sequence
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -243,7 +244,7 @@ def ae_prefill_prompts(ctx, args: ae_prefill_prompts_args) -> None:
     _check(lib().ae_prefill_prompts(ctx, ctypes.byref(args)), ctx)
 
 
-_BF16 = _I32 = _I64 = _U8 = None  # torch dtypes: this module imports torch only once tensors are passed
+_BF16 = _I32 = _I64 = _U8 = None  # torch dtypes: this module imports torch only for the operators' tensors
 
 
 def _load_dtypes():
@@ -252,9 +253,10 @@ def _load_dtypes():
     _BF16, _I32, _I64, _U8 = torch.bfloat16, torch.int32, torch.int64, torch.uint8
 
 
-def _current_device() -> int:
-    import torch
-    return torch.cuda.current_device()
+def _torch_device() -> Optional[int]:
+    """The current device where this process uses torch with a GPU, else None."""
+    torch = sys.modules.get("torch")
+    return torch.cuda.current_device() if torch is not None and torch.cuda.is_available() else None
 
 
 def _rows(name: str, t, width: int, device: int, rows: int = -1):
@@ -380,12 +382,20 @@ class ActionExpert:
         self.dims = dims
         self.config = make_config(dims, dtype, fp8_weights)
         self._wstruct = make_weights(weights)
-        _load_dtypes()
         self._q_dim, self._kv_dim = dims.n_q_heads * dims.head_dim, dims.n_kv_heads * dims.head_dim
         self.ctx = ae_create(self.config, self._wstruct, max_batch, max_prefix_rows, stream)
-        self._device = _current_device()  # the context's, as ae_create takes it
+        self._device = _torch_device()  # the context's, as ae_create takes it; None: not known
         self._axis_array = ctypes.c_uint8 * (dims.head_dim // 2)
         self._bound = None
+
+    def _tensor_device(self) -> int:
+        """The device an operator's tensors have to be on (the library checks that the context's is current)."""
+        if _BF16 is None:
+            _load_dtypes()
+        if self._device is not None:
+            return self._device
+        import torch
+        return torch.cuda.current_device()
 
     def bind_prefix(self, prefix_k, prefix_v, cu_lens, prefix_mask=None):
         batch = len(cu_lens) - 1
@@ -410,7 +420,7 @@ class ActionExpert:
         positions int32 [tokens] or [axes, tokens]; kv_rows int64 [tokens] or None; pair_axis bytes or a
         sequence of dh / 2 axes; pair_freq a sequence of dh / 2 frequencies.
         """
-        qd, kvd, dh, dev = self._q_dim, self._kv_dim, self.dims.head_dim, self._device
+        qd, kvd, dh, dev = self._q_dim, self._kv_dim, self.dims.head_dim, self._tensor_device()
         axes = positions.shape[0] if positions.dim() == 2 else 1
         pair_axis, freq = _pairs(pair_axis, pair_freq, dh // 2)
         x, x_stride, n = _rows("qkv", qkv, qd + 2 * kvd, dev)
@@ -440,7 +450,7 @@ class ActionExpert:
         for name, x in (("kv_row0", row0), ("kv_len", lens)):
             if x is not None and len(x) != batch:
                 raise ValueError(f"{name}: {len(x)} entries for {batch} sequences")
-        dev = self._device
+        dev = self._tensor_device()
         qp, q_stride, rows = _rows("q", q, self._q_dim, dev)
         if rows < cu[batch]:
             raise ValueError(f"q: {rows} rows, cu_q ends at {cu[batch]}")
@@ -462,7 +472,7 @@ class ActionExpert:
         """
         if out is None:
             out = q.new_empty(q.shape)
-        dev = self._device
+        dev = self._tensor_device()
         qp, q_stride, n = _rows("q", q, self._q_dim, dev)
         kp, k_stride, cache_rows = _rows("k", k, self._kv_dim, dev)
         vp, v_stride, _ = _rows("v", v, self._kv_dim, dev, cache_rows)
@@ -481,7 +491,7 @@ class ActionExpert:
         embeddings [total, width] bf16; positions int32 [total] or [axes, total]; out_k / out_v
         [layers, total, Hkv dh] bf16; q_norm / k_norm one bf16 [dh] tensor a layer.
         """
-        d, dev = self.dims, self._device
+        d, dev = self.dims, self._tensor_device()
         cu = _host_array(ctypes.c_int32, cu_lens)
         n = embeddings.shape[0]
         if cu[len(cu) - 1] != n:

@@ -64,3 +64,55 @@ def test_rotation_in_place_takes_any_token_count(host, expert, tokens):
     at = host.host_rope_rows(ctypes.byref(q_stride), ctypes.byref(qkv_stride))
     assert at == qkv.data_ptr()
     assert tokens == 1 or q_stride.value == qkv_stride.value == QD + 2 * KVD
+
+
+def _raw_weights(dims):
+    """Weights as plain addresses (nothing reads them here)."""
+    from flow_matching_action_gb300 import synth
+    w = {n: 0x10000 for n, _ in synth.global_weight_shapes(dims)}
+    for n, _ in synth.layer_weight_shapes(dims):
+        w[n] = [0x10000] * dims.layers
+    return w
+
+
+@pytest.mark.parametrize("torch_there", [False, True])
+def test_a_context_of_plain_addresses_needs_no_torch(host, monkeypatch, torch_there):
+    """Create, bind and sample take addresses: no torch, or one without a GPU, does not matter."""
+    import sys
+
+    import torch
+
+    from flow_matching_action_gb300 import synth
+    calls = []
+    if torch_there:  # a build without CUDA
+        def fail():
+            raise AssertionError("Torch not compiled with CUDA enabled")
+        monkeypatch.setattr(torch.cuda, "is_available", lambda: False)
+        monkeypatch.setattr(torch.cuda, "current_device", fail)
+    else:
+        monkeypatch.setitem(sys.modules, "torch", None)  # an import of it fails
+    monkeypatch.setattr(ae, "ae_create", lambda *a: ctypes.c_void_p(None))
+    monkeypatch.setattr(ae, "ae_bind_prefix", lambda *a: calls.append("bind"))
+    monkeypatch.setattr(ae, "ae_sample", lambda *a: calls.append("sample"))
+    dims = synth.ExpertDims(layers=1, width=128, mlp=128, n_q_heads=HQ, n_kv_heads=HKV, head_dim=DH, horizon=1,
+                            action_dim=8, dtype="bf16")
+    ex = ae.ActionExpert(dims, _raw_weights(dims), 1, 4)
+    ex.bind_prefix(0x10000, 0x10000, [0, 4])
+    assert ex.sample(0x10000, 1, out=0x20000) == 0x20000 and calls == ["bind", "sample"]
+
+
+def test_operators_find_the_device_when_the_constructor_could_not(host, expert, monkeypatch):
+    """A context made before torch was there: its tensors' device is the current one, looked up at each call."""
+    import torch
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
+    expert._device = None
+    before = host.host_launches()
+    x = bf16(3, QD)
+    k = bf16(8, KVD)
+    expert.prompt_attention(x, k, k, [0, 3])
+    expert.token_attention(x, k, k, torch.zeros(3, dtype=torch.int64), torch.ones(3, dtype=torch.int32), 8)
+    expert.qk_norm_rope(bf16(3, QD + 2 * KVD), torch.zeros(3, dtype=torch.int32), x, k, k)
+    assert host.host_launches() == before + 3
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError, match="cuda:1"):
+        expert.prompt_attention(x, k, k, [0, 3])
