@@ -39,6 +39,15 @@ ae_status check_rows(ae_ctx* c, const char* name, const void* p, int64_t stride,
   return AE_OK;
 }
 
+// Written over its input, a row must land on itself (one row does, whatever the
+// strides are): on another row it would replace what is still to be read.
+ae_status check_in_place(ae_ctx* c, const char* out_name, const void* out, int64_t out_stride, const char* in_name,
+                         const void* in, int64_t in_stride, int rows) {
+  if (out == in && rows > 1 && out_stride != in_stride)
+    return fail(c, AE_ERR_INVALID_ARG, "%s is %s but the row strides differ", out_name, in_name);
+  return AE_OK;
+}
+
 // Row counts travel as 32-bit TMA coordinates.
 ae_status check_cache_rows(ae_ctx* c, int64_t rows) {
   if (rows < 0 || rows > 0x7fffff00LL)
@@ -136,9 +145,7 @@ ae_status ae_qk_norm_rope(ae_ctx* c, const ae_qk_norm_rope_args* p) {
   AE_TRY(check_rows(c, "q_out", p->q_out, p->q_stride, d.qdim()));
   AE_TRY(check_rows(c, "k_cache", p->k_cache, p->kv_stride, d.kvdim()));
   AE_TRY(check_rows(c, "v_cache", p->v_cache, p->kv_stride, d.kvdim()));
-  // in place, a row must land on itself (one row does, whatever its strides are)
-  if (p->q_out == p->qkv && p->tokens > 1 && p->q_stride != p->qkv_stride)
-    return fail(c, AE_ERR_INVALID_ARG, "q_out is qkv but the row strides differ");
+  AE_TRY(check_in_place(c, "q_out", p->q_out, p->q_stride, "qkv", p->qkv, p->qkv_stride, p->tokens));
   for (const void* w : {p->q_norm, p->k_norm})
     if ((uintptr_t)w % 16 != 0) return fail(c, AE_ERR_INVALID_ARG, "a norm weight is not 16-byte aligned");
   if (p->positions == nullptr) return fail(c, AE_ERR_INVALID_ARG, "positions is NULL");
@@ -206,6 +213,7 @@ ae_status ae_prompt_attention(ae_ctx* c, const ae_prompt_attention_args* p) {
     return fail(c, AE_ERR_SHAPE, "%d query rows are too many", total);
   AE_TRY(check_rows(c, "q", p->q, p->q_stride, d.qdim()));
   AE_TRY(check_rows(c, "out", p->out, p->out_stride, d.qdim()));
+  AE_TRY(check_in_place(c, "out", p->out, p->out_stride, "q", p->q, p->q_stride, total));
   AE_TRY(check_rows(c, "k", p->k, p->kv_stride, d.kvdim()));
   AE_TRY(check_rows(c, "v", p->v, p->kv_stride, d.kvdim()));
   AE_TRY(check_device(c));
@@ -244,6 +252,7 @@ ae_status ae_token_attention(ae_ctx* c, const ae_token_attention_args* p) {
     return fail(c, AE_ERR_INVALID_ARG, "kv_row0 / kv_len is not aligned to its elements");
   AE_TRY(check_rows(c, "q", p->q, p->q_stride, d.qdim()));
   AE_TRY(check_rows(c, "out", p->out, p->out_stride, d.qdim()));
+  AE_TRY(check_in_place(c, "out", p->out, p->out_stride, "q", p->q, p->q_stride, p->batch));
   if (p->cache_rows > 0) {
     AE_TRY(check_rows(c, "k", p->k, p->kv_stride, d.kvdim()));
     AE_TRY(check_rows(c, "v", p->v, p->kv_stride, d.kvdim()));

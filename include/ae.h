@@ -329,7 +329,8 @@ AE_API ae_status ae_qk_norm_rope(ae_ctx* ctx, const ae_qk_norm_rope_args* args);
  * rows may hold anything (NaN included), rows outside the sequences too; the
  * unmasked rows of a sequence must be finite (a non-finite value row may reach
  * every query of its sequence), and so must its scores in fp32.  out may be q
- * with out_stride == q_stride.
+ * with out_stride == q_stride (AE_ERR_INVALID_ARG with another, for more than
+ * one row).
  */
 typedef struct {
   int batch;                 /* sequences, 0..AE_MAX_BATCH                       */
@@ -355,8 +356,9 @@ AE_API ae_status ae_prompt_attention(ae_ctx* ctx, const ae_prompt_attention_args
  * masked ones, all of them (the new token's own K and V are already stored).
  * Lengths and first rows are read on the device, so a captured graph follows
  * them as they grow.  Formula, mask, finiteness and empty rows as in
- * ae_prompt_attention, and out may be q.  A length above max_len, or a range outside the cache,
- * is cut to what is inside and the context's status becomes AE_ERR_DEVICE.
+ * ae_prompt_attention, and out may be q in the same way.  A length above max_len,
+ * or a range outside the cache, is cut to what is inside and the context's status
+ * becomes AE_ERR_DEVICE.
  */
 typedef struct {
   int batch;                 /* requests, 0..AE_MAX_TOKENS                       */

@@ -116,3 +116,25 @@ def test_operators_find_the_device_when_the_constructor_could_not(host, expert, 
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     with pytest.raises(ValueError, match="cuda:1"):
         expert.prompt_attention(x, k, k, [0, 3])
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("stride", [QD, QD + 8, 2 * QD])
+def test_attention_over_the_queries_keeps_their_stride(host, expert, rows, stride):
+    """With out == q and another stride an output row would land on a query row that is still to be read."""
+    import torch
+    q = torch.zeros(rows * 2 * QD, dtype=torch.bfloat16)
+    k = bf16(8, KVD)
+    row0, lens = torch.zeros(rows, dtype=torch.int64), torch.ones(rows, dtype=torch.int32)
+    wide, over = q.as_strided((rows, QD), (QD + 8, 1)), q.as_strided((rows, QD), (stride, 1))
+    calls = [lambda out: expert.prompt_attention(wide, k, k, [0, rows], out=out),
+             lambda out: expert.token_attention(wide, k, k, row0, lens, 8, out=out)]
+    for call in calls:
+        before = host.host_launches()
+        if rows == 1 or stride == QD + 8:
+            call(over)
+            assert host.host_launches() == before + 1
+        else:
+            with pytest.raises(ae.AEError, match="strides differ") as e:
+                call(over)
+            assert e.value.status == -1 and host.host_launches() == before
