@@ -111,18 +111,20 @@ ae_status launched(ae_ctx* c, cudaError_t e, const char* op) {
 namespace ae {
 
 uint64_t turn_fraction(double radians) {
-  // 1 / (2 pi) as the sum of two doubles: the product is good to 2^-64 of a turn
-  // for every frequency up to 2^40
+  // 1 / (2 pi) as the sum of two doubles: the product is good to 2^-63 of a turn for
+  // every frequency up to 2^30 radians.  Of the magnitude, the sign last: dropping the
+  // whole turns of a negative product near zero would round it (to 2^-54 of a turn).
   const double hi = 0x1.45f306dc9c883p-3, lo = -0x1.6b01ec5417056p-57;
-  const double turns = radians * hi;
-  const double frac = turns - floor(turns);  // whole turns drop out; exact
-  double rest = fma(radians, hi, -turns) + radians * lo;
+  const double r = fabs(radians), turns = r * hi;
+  const double frac = turns - floor(turns);  // exact, in [0, 1)
+  double rest = fma(r, hi, -turns) + r * lo;
   rest -= rint(rest);
   if (rest >= 0.5) rest -= 1.0;
-  // frac in [0, 1]; 2^64 itself wraps to 0
   const double top = floor(frac * 4294967296.0);
   const double low = (frac * 4294967296.0 - top) * 4294967296.0;
-  return ((uint64_t)top << 32) + (uint64_t)low + (uint64_t)(int64_t)(rest * 18446744073709551616.0);
+  const uint64_t t =
+      ((uint64_t)top << 32) + (uint64_t)low + (uint64_t)(int64_t)(rest * 18446744073709551616.0);
+  return radians < 0 ? 0 - t : t;
 }
 
 }  // namespace ae

@@ -1,8 +1,10 @@
 """Calls that the language-model operators take, through the binding and the entry points, on launches
 that only record their arguments (CPU tensors, no GPU)."""
 import ctypes
+import math
 import os
 import subprocess
+from fractions import Fraction
 
 import pytest
 
@@ -138,3 +140,23 @@ def test_attention_over_the_queries_keeps_their_stride(host, expert, rows, strid
             with pytest.raises(ae.AEError, match="strides differ") as e:
                 call(over)
             assert e.value.status == -1 and host.host_launches() == before
+
+
+TWO_PI = 2 * Fraction(314159265358979323846264338327950288419716939937510582097494459230781640628620899, 10 ** 80)
+FREQUENCIES = [0.0, 1.0, 0.3, 1e-3, 1e-4, 3.7e-9, 2.0 ** -60, 0.5, math.pi, 2 * math.pi, 6.283185307179587, 100.7,
+               12345.678, 2.0 ** 30]
+
+
+@pytest.mark.parametrize("f", FREQUENCIES + [-f for f in FREQUENCIES[1:]])
+def test_frequencies_are_fractions_of_a_turn_to_64_bits(host, f):
+    """radians / 2 pi modulo one turn in units of 2^-64, against 80 digits of pi.
+
+    1 / (2 pi) is held as the sum of two doubles, off by less than 2^-110; the fraction's and the remainder's
+    conversions each cut less than one unit, and the remainder (at most 2^-53 of the turns, so 2^-26 of a turn
+    at 2^30 radians) is off by its own rounding of 2^-53: 2^-79 turns.  Two units in all, and 2^-110 times the
+    turns (2^28 at most: 2^-82)."""
+    host.host_turn_fraction.restype = ctypes.c_uint64
+    host.host_turn_fraction.argtypes = [ctypes.c_double]
+    want = Fraction(f) / TWO_PI % 1 * 2 ** 64
+    off = (host.host_turn_fraction(f) - want) % 2 ** 64
+    assert min(off, 2 ** 64 - off) <= 2, float(min(off, 2 ** 64 - off))
