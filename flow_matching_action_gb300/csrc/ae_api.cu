@@ -404,11 +404,22 @@ ae_status sticky(const ae_ctx* c) {
 }  // namespace
 
 namespace ae {
-ae_status ensure_time_table(ae_ctx* c, int n_steps, const TimeTable** out) { return get_table(c, n_steps, out); }
 const TimeTable* find_time_table(const ae_ctx* c, int n_steps) {
   for (const TimeTable& t : c->tables)
     if (t.n_steps == n_steps) return &t;
   return nullptr;
+}
+// A table built inside a capture would break it (the allocations), or be filled
+// only by replays of that graph and found unfilled by every other call.
+ae_status ensure_time_table(ae_ctx* c, int n_steps, const TimeTable** out) {
+  if (find_time_table(c, n_steps) == nullptr) {
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    AE_CK(c, cudaStreamIsCapturing(c->stream, &cap));
+    if (cap != cudaStreamCaptureStatusNone)
+      return set_msg(c, AE_ERR_NOT_BOUND,
+                     "no time-conditioning table yet: make the first call outside of a capture (it builds the table)");
+  }
+  return get_table(c, n_steps, out);
 }
 }  // namespace ae
 

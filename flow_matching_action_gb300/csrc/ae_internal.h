@@ -440,7 +440,8 @@ struct PrefillOut {
 int launch_step_fast(ae_ctx* c, const TimeTable& t, int step, float* x, cudaStream_t s,
                      cudaError_t* err, const AttnScratch* attn_scratch = nullptr,
                      const PrefillOut* prefill = nullptr);
-// The time table of n_steps, built on first use (allocates).
+// The time table of n_steps, built on first use (allocates; AE_ERR_NOT_BOUND while the
+// stream captures).
 ae_status ensure_time_table(ae_ctx* c, int n_steps, const TimeTable** out);
 // The cached time table of n_steps, or nullptr (never allocates).
 const TimeTable* find_time_table(const ae_ctx* c, int n_steps);

@@ -58,7 +58,7 @@ typedef enum {
   AE_OK = 0,
   AE_ERR_INVALID_ARG = -1, /* null pointer, non-positive size, bad enum     */
   AE_ERR_SHAPE = -2,       /* a size outside what the context supports      */
-  AE_ERR_NOT_BOUND = -3,   /* ae_sample before a successful ae_bind_prefix  */
+  AE_ERR_NOT_BOUND = -3,   /* a call before the one that it builds on       */
   AE_ERR_CUDA = -4,        /* a CUDA runtime call failed (see ae_last_error) */
   AE_ERR_DEVICE = -5,      /* a device-side check failed (sticky)           */
   AE_ERR_OOM = -6,         /* device memory allocation failed               */
@@ -261,23 +261,24 @@ AE_API ae_status ae_prefill(ae_ctx* ctx, int batch, const void* embeddings, void
  * over the same KV the action expert reads).  ae_prefill_prompts runs the
  * context's layers with the first two.
  *
- * Common to the operators:
+ * Common to the three operators and ae_prefill_prompts:
  *   - bf16 contexts only (AE_ERR_UNSUPPORTED otherwise), called while the
- *     context's device is current (AE_ERR_INVALID_ARG otherwise).  They use
- *     none of the context's scratch and no workspace, allocate nothing, and
- *     may be captured into a CUDA graph: calls of one context on different
- *     streams (ae_set_stream between them) and replays of several graphs may
- *     overlap as long as their outputs do not.  Host arrays are read before
- *     the call returns (a captured graph keeps the values of the capture).
+ *     context's device is current (AE_ERR_INVALID_ARG otherwise).  Host arrays
+ *     are read before the call returns (a captured graph keeps the values of
+ *     the capture).  Every bf16 pointer is 16-byte aligned (AE_ERR_INVALID_ARG
+ *     otherwise).  Every call with the same arguments gives the same bits.
+ * Common to ae_qk_norm_rope, ae_prompt_attention and ae_token_attention:
+ *   - They use none of the context's scratch and no workspace, allocate
+ *     nothing, and may be captured into a CUDA graph: calls of one context on
+ *     different streams (ae_set_stream between them) and replays of several
+ *     graphs may overlap as long as their outputs do not.
  *   - A row stride is in elements, at least the row's length and a multiple of
- *     8; every bf16 pointer is 16-byte aligned (AE_ERR_INVALID_ARG otherwise).
- *     Row indices times strides may exceed 32 bits.
+ *     8.  Row indices times strides may exceed 32 bits.
  *   - Elements of a row beyond its heads, rows no sequence or token names, and
  *     cache rows not written are left as they were.
  *   - Outputs do not depend on the other sequences or tokens of a call except
  *     through the split of long key ranges (ae_prompt_attention,
- *     ae_token_attention), which changes the order of fp32 sums.  Every call
- *     with the same arguments gives the same bits.
+ *     ae_token_attention), which changes the order of fp32 sums.
  */
 
 /*
@@ -388,11 +389,16 @@ AE_API ae_status ae_token_attention(ae_ctx* ctx, const ae_token_attention_args* 
  * and rotated at the given positions; K (rotated) and V of every layer go to
  * out_k / out_v in the packed layout ae_bind_prefix, ae_prompt_attention and
  * ae_token_attention read.  The projections are rounded to bf16 before the norm.
- * The binding of the context is left as it is.  Allocates the conditioning
- * table on the context's first prefill only.
+ * The binding of the context is left as it is.
+ * Unlike the three operators it works in the context's scratch, as ae_sample and
+ * ae_prefill do: calls and graph replays of these on one context must be ordered
+ * (one stream, or events between streams), never overlap.  The context's first
+ * prefill (or ae_sample with n_steps 1) builds the conditioning table, which
+ * allocates: make it outside of a stream capture.  Later ones may be captured.
  * Errors: AE_ERR_UNSUPPORTED (fp32 context), AE_ERR_SHAPE (batch outside
  * 0..AE_MAX_BATCH, more than max_batch * horizon tokens, bad cu_lens or axes),
- * AE_ERR_INVALID_ARG, AE_ERR_DEVICE, AE_ERR_OOM, AE_ERR_CUDA.
+ * AE_ERR_INVALID_ARG, AE_ERR_NOT_BOUND (the first one, inside a capture),
+ * AE_ERR_DEVICE, AE_ERR_OOM, AE_ERR_CUDA.
  */
 typedef struct {
   int batch;
