@@ -547,7 +547,7 @@ ae_status ae_create(const ae_config* cfg, const ae_weights* w, int max_batch,
     e = ae::fast_setup(c);
     if (e == cudaSuccess) e = ae::gemm_kernel_setup();
     if (e == cudaSuccess) e = ae::attn_kernel_setup();
-    if (e == cudaSuccess) e = ae::prompt_kernel_setup();
+    if (e == cudaSuccess) e = ae::prompt_kernel_setup(c->d.dh, c->prompt_resident);
     if (e == cudaSuccess) e = ae::token_kernel_setup();
     if (e == cudaSuccess) e = cudaStreamCreateWithFlags(&c->cap_stream, cudaStreamNonBlocking);
     if (e != cudaSuccess) st = cuda_fail(c, e, "bf16 path setup");

@@ -294,7 +294,7 @@ int launch_step_fast(ae_ctx* c, const TimeTable& t, int step, float* x, cudaStre
       PromptAttnArgs& p = *prefill->attn;
       p.k = prefill->rope->k_cache;
       p.v = prefill->rope->v_cache;
-      ck(launch_prompt_attention(p, d.dh, s));
+      ck(launch_prompt_attention(p, d.dh, c->prompt_resident, s));
       ++n;
     } else {
       // attention over [valid prefix || actions]

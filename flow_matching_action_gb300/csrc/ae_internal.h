@@ -115,6 +115,7 @@ struct ae_ctx {
   ae::BindState bind;
 
   std::vector<ae::TimeTable> tables;
+  int prompt_resident[4] = {0};   // clusters of 1, 2, 4, 8 CTAs of ae_prompt_attention that the GPU holds at once
   uint64_t* rope_turn = nullptr;  // [dh/2] rope_theta^(-2j/dh) per position as a fraction of a turn (ae_qk_norm_rope)
 
   // Sticky device status: host-mapped so it can be read without a sync.
@@ -380,8 +381,9 @@ struct PromptAttnArgs {
   int kv_len[AE_MAX_BATCH];
   int64_t kv_row0[AE_MAX_BATCH];
 };
-cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int dh, cudaStream_t s);
-cudaError_t prompt_kernel_setup();
+// resident: see ae_ctx::prompt_resident, which prompt_kernel_setup fills.
+cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int dh, const int (&resident)[4], cudaStream_t s);
+cudaError_t prompt_kernel_setup(int dh, int (&resident)[4]);
 
 struct TokenAttnArgs {
   int batch, max_len, Hq, Hkv;

@@ -234,7 +234,7 @@ ae_status ae_prompt_attention(ae_ctx* c, const ae_prompt_attention_args* p) {
   a.scale = p->scale > 0.f ? p->scale : (float)(1.0 / sqrt((double)d.dh));
   a.out = (ae::bf16*)p->out;
   a.status = c->status_dev;
-  return launched(c, ae::launch_prompt_attention(a, d.dh, c->stream), op);
+  return launched(c, ae::launch_prompt_attention(a, d.dh, c->prompt_resident, c->stream), op);
 }
 
 ae_status ae_token_attention(ae_ctx* c, const ae_token_attention_args* p) {

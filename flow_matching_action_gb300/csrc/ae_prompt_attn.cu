@@ -843,14 +843,10 @@ __global__ void __launch_bounds__(Cfg<DH, NQ>::THREADS, Cfg<DH, NQ>::CTAS)
   }
 }
 
-// Clusters of 1, 2, 4 and 8 CTAs with a SM each that the GPU holds at once, for
-// head_dim 64, 128, 256 (the same for every GPU this library runs on).
-int g_resident[3][4];
-
 // The units of a call and their split; its cost in clocks, negative when there are
-// too many units.
+// too many units.  resident: clusters of 1, 2, 4 and 8 CTAs that the GPU holds at once.
 template <int DH, int NQ>
-double plan(const PromptAttnArgs& a, Launch& L, int& smem, int64_t& units) {
+double plan(const PromptAttnArgs& a, const int (&resident)[4], Launch& L, int& smem, int64_t& units) {
   using C = Cfg<DH, NQ>;
   L.G = a.Hq / a.Hkv;
   L.hc = (L.G + 127) / 128;
@@ -896,7 +892,7 @@ double plan(const PromptAttnArgs& a, Launch& L, int& smem, int64_t& units) {
   smem = C::BYTES;
   L.split = L.vs = 1;
   for (int e = 0; e < 4; ++e) {
-    const int n = 1 << e, clusters = g_resident[DH / 128][e];
+    const int n = 1 << e, clusters = resident[e];
     if (clusters == 0 || longest < 2 * n - 1) continue;
     const bool pairs = C::CTAS == 2 && (n == 1 || units > clusters);
     const double ctas = (double)(clusters << e) * (pairs ? 2 : 1);  // at once
@@ -956,18 +952,18 @@ cudaError_t run(const PromptAttnArgs& a, const Launch& L, int smem, int64_t unit
 }
 
 template <int DH>
-cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
+cudaError_t launch(const PromptAttnArgs& a, const int (&resident)[4], cudaStream_t st) {
   constexpr int NQ = DH == 128 ? 2 : 1;
   Launch L;
   int smem;
   int64_t units;
-  const double cost = plan<DH, NQ>(a, L, smem, units);
+  const double cost = plan<DH, NQ>(a, resident, L, smem, units);
   if (cost < 0) return cudaErrorInvalidConfiguration;
-  if (NQ == 2 && units <= 2 * g_resident[DH / 128][0]) {  // single tiles may fill the SMs better
+  if (NQ == 2 && units <= 2 * resident[0]) {  // single tiles may fill the SMs better
     Launch L1;
     int smem1;
     int64_t units1;
-    const double cost1 = plan<DH, 1>(a, L1, smem1, units1);
+    const double cost1 = plan<DH, 1>(a, resident, L1, smem1, units1);
     if (cost1 >= 0 && cost1 < cost) return run<DH, 1>(a, L1, smem1, units1, st);
   }
   return run<DH, NQ>(a, L, smem, units, st);
@@ -975,14 +971,14 @@ cudaError_t launch(const PromptAttnArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int dh, cudaStream_t s) {
-  if (dh == 64) return launch<64>(a, s);
-  if (dh == 128) return launch<128>(a, s);
-  return launch<256>(a, s);
+cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int dh, const int (&resident)[4], cudaStream_t s) {
+  if (dh == 64) return launch<64>(a, resident, s);
+  if (dh == 128) return launch<128>(a, resident, s);
+  return launch<256>(a, resident, s);
 }
 
 template <int DH, int NQ>
-static cudaError_t setup() {
+static cudaError_t setup(int (&resident)[4]) {
   using C = Cfg<DH, NQ>;
   cudaError_t e = cudaSuccess;
   for (auto kern : {k_prompt_attn<DH, NQ, false>, k_prompt_attn<DH, NQ, true>})
@@ -998,17 +994,16 @@ static cudaError_t setup() {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&g_resident[DH / 128][i], k_prompt_attn<DH, NQ, false>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&resident[i], k_prompt_attn<DH, NQ, false>, &cfg);
   }
   return e;
 }
 
-cudaError_t prompt_kernel_setup() {
-  cudaError_t e = setup<64, 1>();
-  if (e == cudaSuccess) e = setup<128, 1>();
-  if (e == cudaSuccess) e = setup<128, 2>();
-  if (e == cudaSuccess) e = setup<256, 1>();
-  return e;
+cudaError_t prompt_kernel_setup(int dh, int (&resident)[4]) {
+  if (dh == 64) return setup<64, 1>(resident);
+  if (dh == 256) return setup<256, 1>(resident);
+  const cudaError_t e = setup<128, 1>(resident);  // a SM each in single tiles and in pairs: the same counts
+  return e == cudaSuccess ? setup<128, 2>(resident) : e;
 }
 
 }  // namespace ae

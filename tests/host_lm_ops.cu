@@ -18,7 +18,7 @@ static cudaError_t host_device(int* dev) {
 static ae::RopeNormArgs g_rope;
 static ae::PromptAttnArgs g_prompt;
 static ae::TokenAttnArgs g_token;
-static int g_launches;
+static int g_launches, g_clusters;
 
 namespace ae {
 cudaError_t launch_qk_norm_rope(const RopeNormArgs& a, int, int, cudaStream_t) {
@@ -26,8 +26,9 @@ cudaError_t launch_qk_norm_rope(const RopeNormArgs& a, int, int, cudaStream_t) {
   ++g_launches;
   return cudaSuccess;
 }
-cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int, cudaStream_t) {
+cudaError_t launch_prompt_attention(const PromptAttnArgs& a, int, const int (&resident)[4], cudaStream_t) {
   g_prompt = a;
+  g_clusters = resident[0];
   ++g_launches;
   return cudaSuccess;
 }
@@ -59,6 +60,8 @@ HOST_API ae_status ae_last_error(const ae_ctx* c, char* buf, size_t n) {
   }
   return AE_OK;
 }
+HOST_API void host_set_clusters(void* c, int n) { ((ae_ctx*)c)->prompt_resident[0] = n; }
+HOST_API int host_clusters() { return g_clusters; }
 HOST_API int host_launches() { return g_launches; }
 HOST_API const void* host_rope_rows(int64_t* q_stride, int64_t* qkv_stride) {
   *q_stride = g_rope.q_stride;

@@ -160,3 +160,18 @@ def test_frequencies_are_fractions_of_a_turn_to_64_bits(host, f):
     want = Fraction(f) / TWO_PI % 1 * 2 ** 64
     off = (host.host_turn_fraction(f) - want) % 2 ** 64
     assert min(off, 2 ** 64 - off) <= 2, float(min(off, 2 ** 64 - off))
+
+
+def test_the_gpu_s_cluster_counts_are_the_context_s_own(host, expert):
+    """What the split of the keys is chosen by belongs to a context: another one's set-up, perhaps on another
+    thread or GPU, does not change it."""
+    host.host_set_clusters.argtypes = [ctypes.c_void_p, ctypes.c_int]
+    host.host_set_clusters(expert.ctx, 152)
+    other = host.host_context(HQ, HKV, DH)
+    try:
+        host.host_set_clusters(other, 7)
+        q, k = bf16(3, QD), bf16(8, KVD)
+        expert.prompt_attention(q, k, k, [0, 3])
+        assert host.host_clusters() == 152
+    finally:
+        host.host_context_free(other)
