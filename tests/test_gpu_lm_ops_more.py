@@ -36,3 +36,42 @@ def test_rotation_in_place_of_single_tokens(experts, hq, hkv, dh, tokens):  # no
     x = f64(qkv).reshape(tokens, hq + 2 * hkv, dh)
     ref = lm_ops.norm_rope(x[:, :hq], f64(w), 0, 1e-6, f64(pos)[None], [0] * (dh // 2), lm_ops.ladder(10000.0, dh))
     check_rope(f64(q).reshape(tokens, hq, dh), ref, "q")
+
+
+@pytest.mark.parametrize("hq,hkv,dh", [(4, 1, 64), (12, 4, 64), (5, 5, 128), (8, 1, 256)])
+@pytest.mark.parametrize("axes,norm,offset,in_place", [(3, True, 1.0, False), (1, False, 0.0, True),
+                                                       (2, True, 0.0, True)])
+def test_rotation_of_more_tokens_than_warps(experts, hq, hkv, dh, axes, norm, offset, in_place):  # noqa: F811
+    """Every warp of the launch (24 a SM) goes on to a second and some to a third token: the next token's pieces,
+    positions and cache row are fetched under this one's; rows scattered, some not stored."""
+    import torch
+    ex, g = experts(hq, hkv, dh), generator(70 + dh + axes)
+    tokens = 2 * 24 * ex.info()["sm_count"] + 37
+    heads, n_rows = hq + 2 * hkv, tokens + 1001
+    qkv = normal(g, tokens, heads * dh, std=2.0)
+    w = normal(g, 2, dh)
+    pos = torch.randint(-50, 70000, (axes, tokens), generator=g, device="cuda", dtype=torch.int32)
+    rows = torch.randperm(n_rows, generator=g, device="cuda")[:tokens]
+    skipped = torch.rand(tokens, generator=g, device="cuda") < 0.1
+    rows = torch.where(skipped, torch.full_like(rows, -1), rows)
+    over = qkv.clone()
+    q = over[:, :hq * dh] if in_place else torch.zeros((tokens, hq * dh), dtype=torch.bfloat16, device="cuda")
+    k = torch.full((n_rows, hkv * dh), 7.0, dtype=torch.bfloat16, device="cuda")
+    v = torch.full_like(k, 5.0)
+    axis = [j % axes for j in range(dh // 2)]
+    ex.qk_norm_rope(over, pos, q, k, v, q_norm=w[0] if norm else None, k_norm=w[1] if norm else None,
+                    norm_offset=offset, pair_axis=bytes(axis), kv_rows=rows)
+    ex.synchronize()
+    assert torch.equal(over[:, hq * dh:], qkv[:, hq * dh:])
+    kept = np.flatnonzero(~skipped.cpu().numpy())
+    where = rows.cpu().numpy()[kept]
+    p, f = f64(pos), lm_ops.ladder(10000.0, dh)
+    got_q, got_k, got_v = f64(q).reshape(tokens, hq, dh), f64(k), f64(v)
+    x = f64(qkv).reshape(tokens, heads, dh)
+    check_rope(got_q, lm_ops.norm_rope(x[:, :hq], f64(w[0]) if norm else None, offset, 1e-6, p, axis, f), "q")
+    check_rope(got_k[where].reshape(-1, hkv, dh),
+               lm_ops.norm_rope(x[kept, hq:hq + hkv], f64(w[1]) if norm else None, offset, 1e-6, p[:, kept], axis, f),
+               "k")
+    assert (got_v[where].reshape(-1, hkv, dh) == x[kept, hq + hkv:]).all()
+    rest = np.setdiff1d(np.arange(n_rows), where)
+    assert (got_k[rest] == 7.0).all() and (got_v[rest] == 5.0).all()
