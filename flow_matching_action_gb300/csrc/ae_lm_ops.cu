@@ -145,8 +145,10 @@ ae_status ae_qk_norm_rope(ae_ctx* c, const ae_qk_norm_rope_args* p) {
     return fail(c, AE_ERR_SHAPE, "%d tokens, %lld cache rows", p->tokens, (long long)p->cache_rows);
   AE_TRY(check_rows(c, "qkv", p->qkv, p->qkv_stride, d.qkvdim()));
   AE_TRY(check_rows(c, "q_out", p->q_out, p->q_stride, d.qdim()));
-  AE_TRY(check_rows(c, "k_cache", p->k_cache, p->kv_stride, d.kvdim()));
-  AE_TRY(check_rows(c, "v_cache", p->v_cache, p->kv_stride, d.kvdim()));
+  if (p->cache_rows > 0) {  // without rows nothing is stored
+    AE_TRY(check_rows(c, "k_cache", p->k_cache, p->kv_stride, d.kvdim()));
+    AE_TRY(check_rows(c, "v_cache", p->v_cache, p->kv_stride, d.kvdim()));
+  }
   AE_TRY(check_in_place(c, "q_out", p->q_out, p->q_stride, "qkv", p->qkv, p->qkv_stride, p->tokens));
   for (const void* w : {p->q_norm, p->k_norm})
     if ((uintptr_t)w % 16 != 0) return fail(c, AE_ERR_INVALID_ARG, "a norm weight is not 16-byte aligned");

@@ -307,7 +307,7 @@ typedef struct {
   const int64_t* kv_rows;    /* device [tokens], cache row of every token, distinct; negative: the token's
                                 K and V are not stored; >= cache_rows: not stored, and the context's status
                                 becomes AE_ERR_DEVICE.  NULL: token t goes to row t */
-  int64_t cache_rows;        /* rows of k_cache / v_cache (>= tokens without kv_rows) */
+  int64_t cache_rows;        /* rows of k_cache / v_cache (>= tokens without kv_rows); 0: they may be NULL */
   void* q_out;               /* device bf16 [tokens][Hq dh]; may be qkv with q_stride == qkv_stride (in place;
                                 one token: any strides) */
   int64_t q_stride;

@@ -75,3 +75,19 @@ def test_rotation_of_more_tokens_than_warps(experts, hq, hkv, dh, axes, norm, of
     assert (got_v[where].reshape(-1, hkv, dh) == x[kept, hq + hkv:]).all()
     rest = np.setdiff1d(np.arange(n_rows), where)
     assert (got_k[rest] == 7.0).all() and (got_v[rest] == 5.0).all()
+
+
+def test_rotation_without_a_cache_row(experts):  # noqa: F811
+    """Queries alone are rotated: no token has a cache row, and there is no cache."""
+    import torch
+    hq, hkv, dh, n = 12, 4, 64, 19
+    ex, g = experts(hq, hkv, dh), generator(80)
+    qkv = normal(g, n, (hq + 2 * hkv) * dh)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    want, q = [torch.empty((n, hq * dh), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    k = torch.zeros((n, hkv * dh), dtype=torch.bfloat16, device="cuda")
+    ex.qk_norm_rope(qkv, pos, want, k, torch.empty_like(k))
+    none = k[:0]
+    ex.qk_norm_rope(qkv, pos, q, none, none, kv_rows=torch.full((n,), -1, dtype=torch.int64, device="cuda"))
+    ex.synchronize()
+    assert torch.equal(q, want)

@@ -175,3 +175,15 @@ def test_the_gpu_s_cluster_counts_are_the_context_s_own(host, expert):
         assert host.host_clusters() == 152
     finally:
         host.host_context_free(other)
+
+
+def test_rotation_without_a_cache_row(host, expert):
+    """No token's K and V are stored (all rows negative): a cache without rows, which has no address, will do."""
+    import torch
+    rows = torch.full((3,), -1, dtype=torch.int64)
+    pos, q = torch.zeros(3, dtype=torch.int32), bf16(3, QD)
+    before = host.host_launches()
+    expert.qk_norm_rope(bf16(3, QD + 2 * KVD), pos, q, bf16(0, KVD), bf16(0, KVD), kv_rows=rows)
+    assert host.host_launches() == before + 1
+    with pytest.raises(ae.AEError):  # without kv_rows the tokens need their rows
+        expert.qk_norm_rope(bf16(3, QD + 2 * KVD), pos, q, bf16(0, KVD), bf16(0, KVD))
