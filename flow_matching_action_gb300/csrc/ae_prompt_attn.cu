@@ -16,7 +16,7 @@
 // into a ring of K and V tiles, one warp issues the MMAs.
 //   head_dim 128: two tiles a CTA alternate, one's MMAs under the other's
 //     softmax; a key tile (two query tiles) takes about 2770 clocks, of which
-//     the MMAs 2048.  32768 tokens 32/8/128: 4.8 ms, 1830 TFLOP/s; bound by the
+//     the MMAs 2048.  32768 tokens 32/8/128: 4.8 ms, 1820 TFLOP/s; bound by the
 //     MMA rate, shared memory's bandwidth near it (operands and TMA writes take
 //     2048 clocks a step too).
 //     Where SMs would idle, one tile a CTA with two S buffers, as at 256: a key
@@ -24,13 +24,14 @@
 //     two tiles a CTA, 4096 48.3 against 55.2 with one).
 //   head_dim 256: O fills half of tensor memory; one tile, two S buffers, the
 //     next Q K^T under this softmax; K and V in half tiles so that a ring of five
-//     fits beside Q.  8192 tokens 8/1/256: 150 us, 1830 TFLOP/s.  (Key tiles of
+//     fits beside Q.  8192 tokens 8/1/256: 151 us, 1820 TFLOP/s.  (Key tiles of
 //     64: 191 us, Q K^T of 64 columns is bound by reading Q from shared memory.)
 //   head_dim 64: one tile a CTA and two CTAs a SM, each in the half of tensor
 //     memory, so one's start, end and MMAs run under the other's softmax; key
 //     tiles of 96, the largest of which two score buffers fit beside O, so the
-//     next Q K^T runs under this softmax too.  Bound by a softmax warp's issue and
-//     the exponentials, half of the cycles each.  8192 tokens 12/4/64: 101 us,
+//     next Q K^T runs under this softmax too.  No unit is full (issue 57% of the
+//     cycles, exponentials 46%, tensor pipe 45%): the chain of a softmax warp
+//     bounds it, two of which share a scheduler.  8192 tokens 12/4/64: 101 us,
 //     1020 TFLOP/s.  (Key tiles of 128, one score buffer: 115 us, prompts of one
 //     to 4097 tokens 40.6 against 34.7 us; 100 tokens, which that holds in one
 //     tile, 14.6 against 15.0 us for 64 of them.  Two tiles sharing K and V in one
@@ -38,10 +39,11 @@
 // What the MMAs need most is an issue thread that never waits: they are issued
 // under elect.sync on warp-uniform operands (a plain lane test costs 75 clocks
 // per MMA in register moves: 6.7 ms for the 32768 tokens), and both next slots
-// are awaited before the weights.  Tried and slower: two threads a row (430
-// against 351 us, 8192 tokens 32/8/128), P handed over in halves (493 against
-// 461), persistent CTAs that fetch the next unit's tiles under this one's end
-// (356 against 341).
+// are awaited before the weights.  Tried on earlier states of this kernel and
+// slower, 8192 tokens 32/8/128 (340 us now): two threads a row (430 against 351
+// us), P handed over in halves (493 against 461), persistent CTAs with static
+// shares that fetch the next unit's tiles under this one's end (356 against 341;
+// ragged batches, where starts and ends weigh most, were not tried).
 // A unit's start and end cost about 8500 clocks (first loads and products 5000,
 // output by TMA through the query tile 2400 at 32 bytes a clock); short prompts
 // are bound by them.

@@ -14,8 +14,8 @@
 // 2^-32 turns) become an fp32 part of half a turn: at most 2^-26 turns off.
 // Bound by the bytes of the rows, read once and written once: 32768 tokens
 // 32/8/128 with norms and scattered rows 136 us, 5.9 TB/s (89% of a plain copy);
-// 5003 tokens 12/4/64 without norms 6.9 us, 3.7 TB/s (a launch and one short wave);
-// 12 tokens 8/1/256 2.8 us, a launch.  (A block a token with the angles behind
+// 5003 tokens 12/4/64 without norms 6.5 us, 3.9 TB/s (a launch and one short wave);
+// 12 tokens 8/1/256 2.5 to 4 us, a launch.  (A block a token with the angles behind
 // barriers took 149.5, 10.2 and 10.4 us.)
 // Arithmetic is fp32; a result is rounded once, to the bf16 of the caches.
 #include "ae_internal.h"

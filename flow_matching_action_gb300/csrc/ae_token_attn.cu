@@ -22,9 +22,10 @@
 // dims: one launch, no workspace, sums in a fixed order.  The ranges follow the
 // lengths on the device, whatever the lengths of the capture were.
 // Bound by the bytes of K and V where requests fill the GPU: 64 of 8k keys
-// 32/8/128 293 us, 7.2 TB/s.  Few or short requests are bound by a launch, the
-// first loads, and the two merges: 712 keys 8/1/256 5.5 us; twelve requests of up
-// to 2048 keys, a camera slot masked, 7.7 us (1.4 TB/s).
+// 32/8/128 290 to 298 us, 7.1 TB/s.  Few or short requests are bound by a launch,
+// the first loads, and the two merges: 712 keys 8/1/256 5.6 us; twelve requests of up
+// to 2048 keys, a camera slot masked, 7.7 us (1.4 TB/s).  Groups of nine to sixteen
+// heads (NB = 2): 64 of 8k keys 16/1/128 44.5 us, 5.9 TB/s.
 // Scores, statistics and O are fp32; weights are rounded to bf16 because the
 // tensor cores multiply bf16 (an error of at most 2^-8 of each term), O once.
 #include <math.h>
